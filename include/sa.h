@@ -66,6 +66,8 @@ typedef enum sa_dtype {
 #define SA_DEVFLAG_TIMEOUT 8u          /* a kernel's bounded wait gave up */
 #define SA_DEVFLAG_SMEM_ALIGN 16u      /* a kernel found its shared memory misaligned (no work done) */
 #define SA_DEVFLAG_ACTION_TYPE 32u     /* an action type id >= the producer's n_types */
+#define SA_DEVFLAG_DECAY 64u           /* a head's log decay is positive or NaN */
+#define SA_DEVFLAG_SLOT 128u           /* a state slot past the pool, or taken twice in one step */
 
 /* Opaque handle: the precomputed query Q' for one weight set. */
 typedef struct sa_query_s* sa_query;
@@ -624,6 +626,239 @@ sa_status sa_action_sketch_forward(sa_action act, sa_query q, const void* E, con
                                    const int64_t* offsets, int64_t batch, int64_t total_rows,
                                    float* X_tilde, float* mass, void* workspace,
                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Linear attention with a decay per head, over a ragged batch of histories:
+ * the causal companion of the sketch.  Per user and head, with rows in
+ * order and S_0 the initial state (zeros when none is given):
+ *
+ *     S_t = exp(log_decay_h) S_{t-1} + k_t v_t^T      d_k x d_v state
+ *     o_t = scale S_t^T q_t                           row t counts itself
+ *
+ * so a history of any length is read once and leaves a state of fixed size,
+ * which sa_linear_attention_step advances by one behaviour.
+ *
+ * Element type of q, k, v, out and their gradients: dtype.  SA_BF16: bf16
+ * products with fp32 accumulation on the tensor cores; the weights of a
+ * tile (q . k times the decay) and the copy of the state that outputs are
+ * taken from are rounded to bf16, and the state itself is kept in fp32, its
+ * sums formed from operands split into two bf16 parts.  SA_FP32: fp32
+ * arithmetic on the CUDA cores.
+ *
+ * Common arguments
+ *   q, k, v     device; row t, head h of q starts at q + t * q_row + h *
+ *               q_head elements (d_k of them, adjacent), likewise k, and v
+ *               (d_v of them): slices of a fused projection need no copy.
+ *               Any alignment of the element type; addresses and strides
+ *               that are multiples of 16 bytes take the tensor-core path
+ *   log_decay   device, heads fp32, each <= 0 (0: no decay; -inf: a row
+ *               sees itself only).  A positive or NaN entry raises
+ *               SA_DEVFLAG_DECAY and counts as 0 or as -inf
+ *   offsets     device, int64, batch + 1 entries: offsets[0] == 0,
+ *               non-decreasing, offsets[batch] <= total_rows.  Rows behind
+ *               offsets[batch] belong to nobody: they are not read, and
+ *               their output rows are left as they were
+ *   batch       0 <= batch < 2^21
+ *   total_rows  0 <= total_rows < 2^31 - 256
+ *   max_rows    the longest history, if known, else 0: batches with few and
+ *               long histories are split along the rows, and a bound saves
+ *               splitting.  A history longer than the bound is still exact
+ *   heads       1 <= heads <= 1024
+ *   d_k, d_v    64 or 128 each
+ *   scale       finite, 1e-20 <= |scale| <= 1e20
+ *   workspace   device, 256-byte aligned, at least
+ *               sa_workspace_bytes_linear_attention(...) bytes of the same
+ *               sizes; one call at a time.  Device flags are read with
+ *               sa_read_device_status on it
+ *
+ * Results are bitwise reproducible for the same inputs on the same GPU
+ * model.  Errors: SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED (not sm_100),
+ * SA_ERR_WORKSPACE, SA_ERR_CUDA.
+ */
+size_t sa_workspace_bytes_linear_attention(int heads, int d_k, int d_v, int64_t batch,
+                                           int64_t total_rows, int64_t max_rows);
+
+/*
+ * sa_linear_attention_forward
+ *   initial_state  device, batch x heads x d_k x d_v fp32, or NULL: zeros
+ *   out            device out, total_rows x heads x d_v, dense; must not
+ *                  overlap the inputs
+ *   final_state    device out, batch x heads x d_k x d_v fp32, or NULL;
+ *                  may be initial_state.  A user without rows keeps its
+ *                  initial state
+ * States and out are 16-byte aligned.
+ */
+sa_status sa_linear_attention_forward(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                                      int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                                      int64_t v_head, const float* log_decay,
+                                      const int64_t* offsets, int64_t batch, int64_t total_rows,
+                                      int64_t max_rows, int heads, int d_k, int d_v,
+                                      sa_dtype dtype, float scale, const float* initial_state,
+                                      void* out, float* final_state, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * sa_linear_attention_backward -- the gradients of q, k, v and the initial
+ * state for d_out = dL/d out and d_final_state = dL/d final_state.  The
+ * decay is a constant of the model and gets none.
+ *   d_out            device, strided as q with d_v elements per head
+ *   d_final_state    device, batch x heads x d_k x d_v fp32, or NULL: zeros
+ *   dq, dk, dv       device out, dense, total_rows x heads x d_k (d_k, d_v)
+ *   d_initial_state  device out, batch x heads x d_k x d_v fp32, or NULL
+ * The outputs must not overlap the inputs or one another.
+ */
+sa_status sa_linear_attention_backward(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                                       int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                                       int64_t v_head, const float* log_decay,
+                                       const int64_t* offsets, int64_t batch, int64_t total_rows,
+                                       int64_t max_rows, int heads, int d_k, int d_v,
+                                       sa_dtype dtype, float scale, const float* initial_state,
+                                       const void* d_out, int64_t d_out_row, int64_t d_out_head,
+                                       const float* d_final_state, void* dq, void* dk, void* dv,
+                                       float* d_initial_state, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * sa_linear_attention_step -- one row for each of `batch` stored states,
+ * which are updated in place (fp32 arithmetic):
+ *   S <- exp(log_decay_h) S + k v^T;  out = scale S^T q
+ *   q, k, v       device, strided as above with the batch entry as the row
+ *   slots         device, batch int64, or NULL (entry b uses state b).  A
+ *                 negative slot marks a padded entry: no state is touched
+ *                 and its output is zero.  A slot >= states, and a slot that
+ *                 an earlier entry of the call has, raise SA_DEVFLAG_SLOT
+ *                 and are treated the same way
+ *   states        states in the pool; >= batch without slots
+ *   d_k           1 to 256;  d_v a multiple of 4, 4 to 256
+ *   state         device, states x heads x d_k x d_v fp32, 16-byte aligned
+ *   out           device out, batch x heads x d_v, dense
+ *   device_flags  device uint32 (or NULL): SA_DEVFLAG_DECAY and
+ *                 SA_DEVFLAG_SLOT are OR-ed in
+ */
+sa_status sa_linear_attention_step(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                                   int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                                   int64_t v_head, const float* log_decay, const int64_t* slots,
+                                   int64_t batch, int64_t states, int heads, int d_k, int d_v,
+                                   sa_dtype dtype, float scale, float* state, void* out,
+                                   uint32_t* device_flags, void* stream);
+
+/*
+ * The norms before and after a block, fused with its gate and residual
+ * scale.  Per row of `d` columns:
+ *
+ *     n = norm(block; post_gain, post_bias)     n = block without post_gain
+ *     r = residual + res_scale * act(gate) * n  residual_out
+ *     u = norm(r; pre_gain, pre_bias)           normed: the next block's input
+ *
+ * norm(x; g, b) = g (x - mean) / sqrt(var + eps) + b in the layer form
+ * (biased variance, as sa_refine_update), g x / sqrt(mean(x^2) + eps) + b in
+ * the root-mean-square form.  Arithmetic is fp32; each output is rounded
+ * once, and u is taken from the unrounded r.
+ */
+typedef enum sa_norm_kind { SA_NORM_LAYER = 0, SA_NORM_RMS = 1 } sa_norm_kind;
+typedef enum sa_gate_kind {
+  SA_GATE_IDENTITY = 0, /* act(z) = z */
+  SA_GATE_SIGMOID = 1,  /* act(z) = 1 / (1 + exp(-z)) */
+  SA_GATE_SILU = 2      /* act(z) = z / (1 + exp(-z)) */
+} sa_gate_kind;
+
+/*
+ * sa_block_norm_forward
+ *   residual      device, rows of residual_dtype, ld_residual elements apart
+ *   block         device, rows of dtype, ld_block apart, or NULL: r =
+ *                 residual, only u is computed (the first block's norm)
+ *   gate          device, rows of dtype, ld_gate apart, or NULL: act = 1
+ *   post_gain, post_bias, res_scale, pre_gain, pre_bias
+ *                 device, d fp32 each, or NULL: no norm after the block, no
+ *                 bias, scale 1, no norm before the next block (then normed
+ *                 is NULL), no bias.  A bias needs its gain; gate, post_gain
+ *                 and res_scale need a block
+ *   rows          0 <= rows < 2^40;  d  1 to 8192;  every ld >= d
+ *   residual_dtype, dtype   SA_BF16 or SA_FP32; bf16 residuals need dtype
+ *                 SA_BF16
+ *   eps           positive
+ *   residual_out  device out, rows x d of residual_dtype, dense; NULL if and
+ *                 only if block is; may be residual where that is dense
+ *   normed        device out, rows x d of dtype, dense, NULL if and only if
+ *                 pre_gain is
+ * Rows whose addresses and widths are multiples of 16 bytes run fastest; any
+ * others are taken element by element.
+ */
+sa_status sa_block_norm_forward(const void* residual, int64_t ld_residual, const void* block,
+                                int64_t ld_block, const void* gate, int64_t ld_gate,
+                                const float* post_gain, const float* post_bias,
+                                const float* res_scale, const float* pre_gain,
+                                const float* pre_bias, int64_t rows, int d,
+                                sa_dtype residual_dtype, sa_dtype dtype, sa_norm_kind kind,
+                                sa_gate_kind gate_kind, float eps, void* residual_out,
+                                void* normed, void* stream);
+
+/*
+ * sa_block_norm_backward -- the gradients, at the forward's residual_out.
+ * Nothing is saved by the forward: the statistics are taken again.
+ *   residual_out        the forward's output r (read only with d_normed)
+ *   block, gate, gains, scale, kinds, eps   as in the forward
+ *   d_residual_out      device, rows of residual_dtype, ld_d_residual apart:
+ *                       dL/dr from what else reads r, or NULL: zeros
+ *   d_normed            device, rows of dtype, ld_d_normed apart: dL/du;
+ *                       NULL if and only if pre_gain is
+ *   d_residual          device out, rows x d of residual_dtype, dense; may
+ *                       be d_residual_out where that is dense
+ *   d_block, d_gate     device out, rows x d of dtype, dense; NULL if and
+ *                       only if block (gate) is
+ *   d_post_gain, d_post_bias, d_res_scale, d_pre_gain, d_pre_bias
+ *                       device out, d fp32, the sums over the rows, each or
+ *                       NULL; zeros for rows == 0
+ *   workspace           device, 16-byte aligned, at least
+ *                       sa_workspace_bytes_block_norm(rows, d) bytes; may be
+ *                       NULL when none of those sums is asked for
+ * The sums are added in a fixed order: bitwise reproducible.
+ */
+size_t sa_workspace_bytes_block_norm(int64_t rows, int d);
+sa_status sa_block_norm_backward(const void* residual_out, int64_t ld_residual, const void* block,
+                                 int64_t ld_block, const void* gate, int64_t ld_gate,
+                                 const float* post_gain, const float* post_bias,
+                                 const float* res_scale, const float* pre_gain, int64_t rows,
+                                 int d, sa_dtype residual_dtype, sa_dtype dtype,
+                                 sa_norm_kind kind, sa_gate_kind gate_kind, float eps,
+                                 const void* d_residual_out, int64_t ld_d_residual,
+                                 const void* d_normed, int64_t ld_d_normed, void* d_residual,
+                                 void* d_block, void* d_gate, float* d_post_gain,
+                                 float* d_post_bias, float* d_res_scale, float* d_pre_gain,
+                                 float* d_pre_bias, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * The global gradient norm over many tensors, and clipping by it:
+ *
+ *     norm = sqrt(sum of g^2 over all elements of all tensors)
+ *     out  = g * min(1, max_norm / (norm + 1e-6))
+ *
+ *   grads       host array of `tensors` device addresses; tensor i holds
+ *               numel[i] (host) adjacent elements of dtypes[i] (host).  The
+ *               arrays are read before the call returns and nothing is kept;
+ *               a captured call keeps the addresses it was captured with
+ *   tensors     0 <= tensors <= 2^20; empty tensors are allowed
+ *   norm        device out, one fp32
+ *   workspace   device, 8-byte aligned, at least
+ *               sa_workspace_bytes_grad_norm(tensors) bytes
+ *   out         host array of device addresses (sizes and types of grads),
+ *               or NULL: in place.  No written tensor may overlap another
+ *               tensor of the call, so a tensor listed twice is refused;
+ *               out[i] may be grads[i]
+ *   max_norm    finite, >= 0
+ *
+ * Squares are summed in fp64 over the whole range of fp32, in a fixed order
+ * (bitwise reproducible).  If the norm is not finite the values are left
+ * (copied) as they are and *norm says so.
+ */
+size_t sa_workspace_bytes_grad_norm(int64_t tensors);
+sa_status sa_grad_norm(const void* const* grads, const int64_t* numel, const sa_dtype* dtypes,
+                       int64_t tensors, float* norm, void* workspace, size_t workspace_bytes,
+                       void* stream);
+sa_status sa_clip_grad_norm(void* const* grads, void* const* out, const int64_t* numel,
+                            const sa_dtype* dtypes, int64_t tensors, float max_norm, float* norm,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* sa_status_string(sa_status s);

@@ -29,3 +29,9 @@ from .sa_refine import (  # noqa: F401
     swiglu_ffn,
 )
 from .sa_action import action_fuse, fusion_hidden, fusion_input  # noqa: F401
+from .block_norm import block_norm, block_norm_grad  # noqa: F401
+from .linear_attention import (  # noqa: F401
+    linear_attention,
+    linear_attention_grad,
+    linear_attention_step,
+)

@@ -16,6 +16,13 @@ from .binding import (  # noqa: F401
     SketchCache,
     SketchQuery,
     WidthAdapter,
+    block_norm_backward,
+    block_norm_forward,
+    clip_grad_norm,
+    grad_norm,
+    linear_attention_backward,
+    linear_attention_forward,
+    linear_attention_step,
     load_library,
     mass_normalise,
     read_device_status,

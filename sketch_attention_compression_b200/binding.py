@@ -20,11 +20,15 @@ SA_OK, SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_WORKSPACE, SA_ERR_CUDA, \
     SA_ERR_DEVICE_FLAG = range(6)
 SA_BF16, SA_FP32 = 0, 1
 DEVFLAG_OFFSET0_NONZERO, DEVFLAG_OFFSETS_DECREASE, DEVFLAG_OFFSET_LAST, DEVFLAG_TIMEOUT, \
-    DEVFLAG_SMEM_ALIGN, DEVFLAG_ACTION_TYPE = 1, 2, 4, 8, 16, 32
+    DEVFLAG_SMEM_ALIGN, DEVFLAG_ACTION_TYPE, DEVFLAG_DECAY, DEVFLAG_SLOT = \
+    1, 2, 4, 8, 16, 32, 64, 128
+SA_NORM_KINDS = {"layer": 0, "rms": 1}
+SA_GATE_KINDS = {"identity": 0, "sigmoid": 1, "silu": 2}
 
 # name -> (restype, argtypes); mirrors include/sa.h
 _vp, _i32, _i64, _sz, _f32, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, \
     ctypes.c_size_t, ctypes.c_float, ctypes.c_double
+_QKV_ARGS = [_vp, _i64, _i64] * 3  # three strided operands
 _FWD_ARGS = [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]
 SIGNATURES = {
     "sa_prepare_query": (_i32, [_vp, _vp, _vp, _i32, _i32, _f32, _i32, _vp,
@@ -73,6 +77,23 @@ SIGNATURES = {
                                  ctypes.POINTER(_vp)]),
     "sa_action_free": (None, [_vp]),
     "sa_action_fuse": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "sa_workspace_bytes_linear_attention": (_sz, [_i32, _i32, _i32, _i64, _i64, _i64]),
+    "sa_linear_attention_forward": (_i32, _QKV_ARGS + [_vp, _vp, _i64, _i64, _i64, _i32, _i32,
+                                                       _i32, _i32, _f32, _vp, _vp, _vp, _vp, _sz,
+                                                       _vp]),
+    "sa_linear_attention_backward": (_i32, _QKV_ARGS + [_vp, _vp, _i64, _i64, _i64, _i32, _i32,
+                                                        _i32, _i32, _f32, _vp, _vp, _i64, _i64,
+                                                        _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sa_linear_attention_step": (_i32, _QKV_ARGS + [_vp, _vp, _i64, _i64, _i32, _i32, _i32, _i32,
+                                                    _f32, _vp, _vp, _vp, _vp]),
+    "sa_block_norm_forward": (_i32, [_vp, _i64] * 3 + [_vp] * 5 + [_i64, _i32, _i32, _i32, _i32, _i32,
+                                                            _f32, _vp, _vp, _vp]),
+    "sa_workspace_bytes_block_norm": (_sz, [_i64, _i32]),
+    "sa_block_norm_backward": (_i32, [_vp, _i64] * 3 + [_vp] * 4 + [
+        _i64, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i64, _vp, _i64] + [_vp] * 9 + [_sz, _vp]),
+    "sa_workspace_bytes_grad_norm": (_sz, [_i64]),
+    "sa_grad_norm": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "sa_clip_grad_norm": (_i32, [_vp, _vp, _vp, _vp, _i64, _f32, _vp, _vp, _sz, _vp]),
     "sa_workspace_bytes_action_sketch": (_sz, [_vp, _i64, _i64]),
     "sa_action_sketch_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz,
                                         _vp]),
@@ -706,3 +727,358 @@ class ActionFusion:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- linear attention
+
+
+def _strided(t, name, heads_shape, dtype):
+    """(pointer, row stride, head stride) of a (rows, heads, d) CUDA tensor
+    whose last dimension is adjacent in memory."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, like q")
+    if tuple(t.shape) != heads_shape:
+        raise ValueError(f"{name} must have shape {heads_shape}")
+    if t.stride(2) != 1 and t.numel() > 0:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr() if t.numel() > 0 else None, t.stride(0), t.stride(1)
+
+
+def _optional(t, name, shape, dtype):
+    """Pointer of a dense CUDA tensor of that shape and type; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {shape}")
+    if t.numel() == 0:
+        return None
+    return _dev_ptr(t, name)
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: every operand must live there."""
+    current = _torch().cuda.current_device() if any(
+        t is not None and t.is_cuda for t in tensors) else -1
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError("every tensor must be on the current CUDA device")
+
+
+def _attention_shapes(q, v):
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be (rows, heads, d)")
+    rows, heads, d_k = (int(x) for x in q.shape)
+    return rows, heads, d_k, int(v.shape[2])
+
+
+def _attention_workspace(lib, workspace, device, *sizes):
+    if workspace is None:
+        workspace = _torch().empty(lib.sa_workspace_bytes_linear_attention(*sizes) or 256,
+                                   dtype=_torch().uint8, device=device)
+    return workspace, _dev_ptr(workspace, "workspace"), \
+        int(workspace.numel() * workspace.element_size())
+
+
+def linear_attention_forward(q, k, v, log_decay, offsets, scale, initial_state=None,
+                             max_rows=None, out=None, final_state=None, workspace=None,
+                             stream=None):
+    """Linear attention with a decay per head over a ragged batch
+    (sa_linear_attention_forward): S_t = exp(log_decay) S_{t-1} + k_t v_t^T,
+    out_t = scale S_t^T q_t.
+
+    q, k (N, H, d_k) and v (N, H, d_v) are CUDA tensors of one dtype (bf16 or
+    fp32), strided as they come as long as the last dimension is contiguous;
+    log_decay (H,) fp32; offsets (B + 1,) int64; initial_state (B, H, d_k,
+    d_v) fp32 or None; max_rows a bound on the longest history, if known.
+    Returns (out (N, H, d_v), final_state (B, H, d_k, d_v) fp32, workspace);
+    final_state may be given as initial_state itself."""
+    torch = _torch()
+    lib = load_library()
+    N, H, dk, dv = _attention_shapes(q, v)
+    if offsets.dtype != torch.int64 or offsets.dim() != 1:
+        raise TypeError("offsets must be a 1-D int64 tensor")
+    B = int(offsets.shape[0]) - 1
+    states = (B, H, dk, dv)
+    args = (*_strided(q, "q", (N, H, dk), q.dtype), *_strided(k, "k", (N, H, dk), q.dtype),
+            *_strided(v, "v", (N, H, dv), q.dtype))
+    if out is None:
+        out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+    if final_state is None:
+        final_state = torch.empty(states, dtype=torch.float32, device=q.device)
+    bound = 0 if max_rows is None else int(max_rows)
+    workspace, wp, wn = _attention_workspace(lib, workspace, q.device, H, dk, dv, B, N, bound)
+    _on_current_device(q, k, v, log_decay, offsets, initial_state, out, final_state, workspace)
+    _check(lib.sa_linear_attention_forward(
+        *args, _optional(log_decay, "log_decay", (H,), torch.float32), _dev_ptr(offsets, "offsets"),
+        B, N, bound, H, dk, dv, _dtype_code(q.dtype), float(scale),
+        _optional(initial_state, "initial_state", states, torch.float32),
+        _optional(out, "out", (N, H, dv), q.dtype),
+        _optional(final_state, "final_state", states, torch.float32), wp, wn,
+        _stream_handle(stream)), "sa_linear_attention_forward")
+    return out, final_state, workspace
+
+
+def linear_attention_backward(q, k, v, log_decay, offsets, scale, d_out, initial_state=None,
+                              d_final_state=None, max_rows=None, workspace=None, stream=None):
+    """Gradients of linear_attention_forward (sa_linear_attention_backward)
+    for d_out = dL/d out (N, H, d_v) and d_final_state = dL/d final_state or
+    None.  Returns dict(dq, dk, dv, and d_initial_state where an initial
+    state is given) and the workspace."""
+    torch = _torch()
+    lib = load_library()
+    N, H, dk, dv = _attention_shapes(q, v)
+    if offsets.dtype != torch.int64 or offsets.dim() != 1:
+        raise TypeError("offsets must be a 1-D int64 tensor")
+    B = int(offsets.shape[0]) - 1
+    states = (B, H, dk, dv)
+    args = (*_strided(q, "q", (N, H, dk), q.dtype), *_strided(k, "k", (N, H, dk), q.dtype),
+            *_strided(v, "v", (N, H, dv), q.dtype))
+    grad = _strided(d_out, "d_out", (N, H, dv), q.dtype)
+    out = dict(dq=torch.empty((N, H, dk), dtype=q.dtype, device=q.device),
+               dk=torch.empty((N, H, dk), dtype=q.dtype, device=q.device),
+               dv=torch.empty((N, H, dv), dtype=q.dtype, device=q.device))
+    if initial_state is not None:
+        out["d_initial_state"] = torch.empty(states, dtype=torch.float32, device=q.device)
+    bound = 0 if max_rows is None else int(max_rows)
+    workspace, wp, wn = _attention_workspace(lib, workspace, q.device, H, dk, dv, B, N, bound)
+    _on_current_device(q, k, v, log_decay, offsets, d_out, initial_state, d_final_state, workspace)
+    _check(lib.sa_linear_attention_backward(
+        *args, _optional(log_decay, "log_decay", (H,), torch.float32), _dev_ptr(offsets, "offsets"),
+        B, N, bound, H, dk, dv, _dtype_code(q.dtype), float(scale),
+        _optional(initial_state, "initial_state", states, torch.float32), *grad,
+        _optional(d_final_state, "d_final_state", states, torch.float32),
+        *(out[x].data_ptr() if N > 0 else None for x in ("dq", "dk", "dv")),
+        out["d_initial_state"].data_ptr() if initial_state is not None else None, wp, wn,
+        _stream_handle(stream)), "sa_linear_attention_backward")
+    return out, workspace
+
+
+def linear_attention_step(state, q, k, v, log_decay, scale, slots=None, out=None,
+                          device_flags=None, stream=None):
+    """One row for each of B stored states (sa_linear_attention_step), which
+    are updated in place.  state (S, H, d_k, d_v) fp32; q, k (B, H, d_k) and
+    v (B, H, d_v) bf16 or fp32; slots (B,) int64: the state of each entry (a
+    negative slot marks a padded entry), or None for entry b's state b.
+    Returns out (B, H, d_v)."""
+    torch = _torch()
+    lib = load_library()
+    B, H, dk, dv = _attention_shapes(q, v)
+    if state.dim() != 4:
+        raise ValueError("state must be (states, heads, d_k, d_v)")
+    if out is None:
+        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+    S = int(state.shape[0])
+    _on_current_device(state, q, k, v, log_decay, slots, out, device_flags)
+    _check(lib.sa_linear_attention_step(
+        *_strided(q, "q", (B, H, dk), q.dtype), *_strided(k, "k", (B, H, dk), q.dtype),
+        *_strided(v, "v", (B, H, dv), q.dtype),
+        _optional(log_decay, "log_decay", (H,), torch.float32),
+        _optional(slots, "slots", (B,), torch.int64), B, S, H, dk, dv, _dtype_code(q.dtype),
+        float(scale), _optional(state, "state", (S, H, dk, dv), torch.float32),
+        _optional(out, "out", (B, H, dv), q.dtype),
+        None if device_flags is None else _dev_ptr(device_flags, "device_flags"),
+        _stream_handle(stream)), "sa_linear_attention_step")
+    return out
+
+
+# ---------------------------------------------------------------- norms around a block
+
+
+def _rows2d(t, name, shape, dtype):
+    """(pointer, row stride) of a tensor of (..., d) rows at one stride."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {shape}")
+    if t.numel() == 0:
+        return t.data_ptr() or 256, shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows")
+    return t.data_ptr(), t.stride(0)
+
+
+def _norm_params(d, kind, gate_kind, **vectors):
+    if kind not in SA_NORM_KINDS or gate_kind not in SA_GATE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(SA_NORM_KINDS)}, gate_kind one of "
+                         f"{sorted(SA_GATE_KINDS)}")
+    f32 = _torch().float32
+    return [_optional(t, name, (d,), f32) for name, t in vectors.items()]
+
+
+def block_norm_forward(residual, block=None, gate=None, post_gain=None, post_bias=None,
+                       res_scale=None, pre_gain=None, pre_bias=None, kind="layer",
+                       gate_kind="identity", eps=1e-5, dtype=None, residual_out=None,
+                       normed=None, stream=None):
+    """The norms around a block with its gate and residual scale
+    (sa_block_norm_forward):
+
+        r = residual + res_scale * act(gate) * norm(block; post_gain, post_bias)
+        u = norm(r; pre_gain, pre_bias)
+
+    residual (..., d) bf16 or fp32; block and gate (..., d) of one dtype (an
+    fp32 residual takes either); the parameters (d,) fp32.  What is None is
+    left out; without a block only u is computed, in `dtype` (the residual's
+    by default).  Returns (r, u), None for what is not computed."""
+    torch = _torch()
+    lib = load_library()
+    shape = tuple(residual.shape)
+    d = int(shape[-1])
+    rows = residual.numel() // d if d > 0 else 0
+    if block is not None:
+        dtype = block.dtype
+    elif dtype is None:
+        dtype = residual.dtype
+    params = _norm_params(d, kind, gate_kind, post_gain=post_gain, post_bias=post_bias,
+                          res_scale=res_scale, pre_gain=pre_gain, pre_bias=pre_bias)
+    if block is not None and residual_out is None:
+        residual_out = torch.empty(shape, dtype=residual.dtype, device=residual.device)
+    if pre_gain is not None and normed is None:
+        normed = torch.empty(shape, dtype=dtype, device=residual.device)
+    _on_current_device(residual, block, gate, post_gain, post_bias, res_scale, pre_gain, pre_bias,
+                       residual_out, normed)
+    _check(lib.sa_block_norm_forward(
+        *_rows2d(residual, "residual", shape, residual.dtype), *_rows2d(block, "block", shape, dtype),
+        *_rows2d(gate, "gate", shape, dtype), *params, rows, d, _dtype_code(residual.dtype),
+        _dtype_code(dtype), SA_NORM_KINDS[kind], SA_GATE_KINDS[gate_kind], float(eps),
+        _dense(residual_out, "residual_out", shape, residual.dtype),
+        _dense(normed, "normed", shape, dtype), _stream_handle(stream)), "sa_block_norm_forward")
+    return residual_out, normed
+
+
+def _dense(t, name, shape, dtype):
+    """Pointer of a dense output; not None for an empty one, which the
+    library takes for an output that is asked for."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {shape}")
+    return _dev_ptr(t, name) if t.numel() > 0 else 256
+
+
+def block_norm_backward(residual_out, block, d_residual_out, d_normed, gate=None, post_gain=None,
+                        post_bias=None, res_scale=None, pre_gain=None, pre_bias=None,
+                        kind="layer", gate_kind="identity", eps=1e-5, dtype=None, workspace=None,
+                        stream=None):
+    """Gradients of block_norm_forward (sa_block_norm_backward) at its output
+    residual_out, for d_residual_out = dL/dr (None: zeros) and d_normed =
+    dL/du (None without a pre_gain).  Returns a dict of d_residual, and of
+    d_block, d_gate, d_post_gain, d_post_bias, d_res_scale, d_pre_gain,
+    d_pre_bias for the operands given."""
+    torch = _torch()
+    lib = load_library()
+    shape = tuple(residual_out.shape)
+    d = int(shape[-1])
+    rows = residual_out.numel() // d if d > 0 else 0
+    tr, dev = residual_out.dtype, residual_out.device
+    if block is not None:
+        dtype = block.dtype
+    elif dtype is None:
+        dtype = tr if d_normed is None else d_normed.dtype
+    params = _norm_params(d, kind, gate_kind, post_gain=post_gain, post_bias=post_bias,
+                          res_scale=res_scale, pre_gain=pre_gain, pre_bias=pre_bias)
+    out = dict(d_residual=torch.empty(shape, dtype=tr, device=dev))
+    for name, t in (("d_block", block), ("d_gate", gate)):
+        if t is not None:
+            out[name] = torch.empty(shape, dtype=dtype, device=dev)
+    sums = []
+    for name, t in (("d_post_gain", post_gain), ("d_post_bias", post_bias),
+                    ("d_res_scale", res_scale), ("d_pre_gain", pre_gain), ("d_pre_bias", pre_bias)):
+        if t is not None:
+            out[name] = torch.empty((d,), dtype=torch.float32, device=dev)
+        sums.append(out[name].data_ptr() if t is not None else None)
+    if workspace is None and any(sums):
+        workspace = torch.empty(lib.sa_workspace_bytes_block_norm(rows, d) or 16, dtype=torch.uint8,
+                                device=dev)
+    _on_current_device(residual_out, block, gate, d_residual_out, d_normed, post_gain, post_bias,
+                       res_scale, pre_gain, pre_bias, workspace)
+    _check(lib.sa_block_norm_backward(
+        *_rows2d(residual_out, "residual_out", shape, tr), *_rows2d(block, "block", shape, dtype),
+        *_rows2d(gate, "gate", shape, dtype), *params[:4], rows, d, _dtype_code(tr),
+        _dtype_code(dtype), SA_NORM_KINDS[kind], SA_GATE_KINDS[gate_kind], float(eps),
+        *_rows2d(d_residual_out, "d_residual_out", shape, tr),
+        *_rows2d(d_normed, "d_normed", shape, dtype),
+        *(_dense(out.get(name), name, shape, t) for name, t in (
+            ("d_residual", tr), ("d_block", dtype), ("d_gate", dtype))), *sums,
+        None if workspace is None else _dev_ptr(workspace, "workspace"),
+        0 if workspace is None else int(workspace.numel() * workspace.element_size()),
+        _stream_handle(stream)), "sa_block_norm_backward")
+    return out
+
+
+# ---------------------------------------------------------------- gradient norm
+
+
+def _tensor_table(tensors, name):
+    """(addresses, sizes, types) of dense CUDA tensors as ctypes arrays."""
+    n = len(tensors)
+    bf16, f32 = _torch().bfloat16, _torch().float32
+    codes = []
+    for t in tensors:
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous CUDA tensors")
+        if t.dtype == bf16:
+            codes.append(SA_BF16)
+        elif t.dtype == f32:
+            codes.append(SA_FP32)
+        else:
+            raise TypeError(f"{name} must be bfloat16 or float32")
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), (ctypes.c_int * n)(*codes))
+
+
+def _norm_buffers(lib, tensors, norm, workspace, device):
+    torch = _torch()
+    if len(tensors) == 0 and device is None:
+        raise ValueError("device is needed when there are no gradients")
+    device = tensors[0].device if len(tensors) > 0 else device
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=device)
+    elif norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must hold one float32")
+    if workspace is None:
+        workspace = torch.empty(lib.sa_workspace_bytes_grad_norm(len(tensors)), dtype=torch.uint8,
+                                device=device)
+    _on_current_device(norm, workspace, *tensors)
+    return norm, (_dev_ptr(norm, "norm"), _dev_ptr(workspace, "workspace"),
+                  int(workspace.numel() * workspace.element_size()))
+
+
+def grad_norm(grads, norm=None, workspace=None, device=None, stream=None):
+    """The global L2 norm of a list of bf16 and fp32 CUDA tensors
+    (sa_grad_norm), as a device scalar."""
+    lib = load_library()
+    grads = list(grads)
+    addresses, sizes, types = _tensor_table(grads, "grads")
+    norm, buffers = _norm_buffers(lib, grads, norm, workspace, device)
+    _check(lib.sa_grad_norm(addresses, sizes, types, len(grads), *buffers, _stream_handle(stream)),
+           "sa_grad_norm")
+    return norm
+
+
+def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, device=None,
+                   stream=None):
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)) of their
+    global norm (sa_clip_grad_norm), in place or into the tensors of `out`,
+    and returns the norm before it as a device scalar.  Where the norm is not
+    finite the values stay as they are."""
+    lib = load_library()
+    grads = list(grads)
+    addresses, sizes, types = _tensor_table(grads, "grads")
+    targets = None
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads) or any(o.shape != g.shape or o.dtype != g.dtype
+                                         for o, g in zip(out, grads)):
+            raise ValueError("out must match grads in number, shapes and types")
+        targets = _tensor_table(out, "out")[0]
+        _on_current_device(*out)
+    norm, buffers = _norm_buffers(lib, grads, norm, workspace, device)
+    _check(lib.sa_clip_grad_norm(addresses, targets, sizes, types, len(grads), float(max_norm),
+                                 *buffers, _stream_handle(stream)), "sa_clip_grad_norm")
+    return norm

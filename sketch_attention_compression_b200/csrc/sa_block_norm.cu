@@ -1,0 +1,698 @@
+// The norms before and after a block, fused with the block's gate and
+// residual scale (the residual stream around a mixing block such as linear
+// attention or the FFN), forward and backward:
+//
+//   n = norm(y; g1, b1)              norm after the block (n = y without g1)
+//   r = x + rs * act(z) * n          residual scale rs, gate act(z)
+//   u = norm(r; g2, b2)              norm before the next block
+//
+// norm(x; g, b) = g (x - mean) rstd + b (layer) or g x rstd + b (root mean
+// square, mean = 0), rstd = 1 / sqrt(var + eps).  Backward, from r, y, z and
+// the upstream gradients dr, du (x^ the normalised value):
+//
+//   h   = du g2;   dx = dr + rstd_r (h - mean(h) - r^ mean(h r^))
+//   dn  = dx rs act(z);   dz = dx rs n act'(z);   drs = sum dx act(z) n
+//   p   = dn g1;   dy = rstd_y (p - mean(p) - y^ mean(p y^))
+//   dg2 = sum du r^, db2 = sum du, dg1 = sum dn y^, db1 = sum dn   (over rows)
+//
+// (mean(h) and mean(p) only in the layer form).  All arithmetic is fp32; an
+// output is rounded once, when it is stored, and u is taken from the
+// unrounded r.  Statistics are two-pass (mean, then squared deviations): the
+// row is in registers, so the second pass costs no memory access and large
+// means lose nothing.
+//
+// What bounds it: memory; each input is read once and each output written
+// once.  A row is held by R threads, 8 columns (one or two 16-byte loads)
+// per thread and operand, so that gains, biases and the backward's five
+// column sums stay in registers over the rows of a persistent block.  R is
+// the power of two that covers d: up to 32, several rows share a warp or
+// block and reduce by shuffles; above, one block holds one row and reduces
+// through shared memory with one barrier per reduction.  The next row's
+// operands are loaded before the current row is reduced, to keep loads in
+// flight across the reductions.  Rows whose width or address does not allow
+// 16-byte accesses use the same code with single-element loads at columns
+// R apart, so that neighbouring threads read neighbouring elements.
+#include <cuda_bf16.h>
+
+#include "sa.h"
+#include "sa_internal.h"
+#include "sa_ptx.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kMaxNormWidth = 8192;
+constexpr int kMaxNormRows = 2;  // 8-column groups per thread at most
+
+struct NormArgs {
+  const void *x, *y, *z;        // forward: residual, block, gate; backward: r, block, gate
+  int64_t ldx, ldy, ldz;
+  const float *g1, *b1, *rs, *g2, *b2;
+  const void *dr, *du;          // backward only
+  int64_t lddr, lddu;
+  void *o1, *o2, *o3;           // forward: r, u; backward: dx, dy, dz
+  float* part;                  // backward: [grid][5][d] column sums
+  int64_t rows;
+  int d, layer, gate_kind, sums;
+  float eps, inv_d;
+};
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f(float v, uint16_t& o) {
+  o = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Eight columns of one operand, as loaded.
+template <class T, bool VEC>
+struct Frag {
+  T v[8];
+  __device__ __forceinline__ void load(const T* row, int l, int j, int R, int d) {
+    if constexpr (VEC) {
+      const int c = (l + j * R) * 8;
+      if (c < d) {
+        const uint4* p = reinterpret_cast<const uint4*>(row + c);
+        uint4* q = reinterpret_cast<uint4*>(v);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) q[i] = p[i];
+        return;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = l + R * (j * 8 + e);
+      v[e] = (!VEC && c < d) ? row[c] : T(0);
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int l, int j, int R, int d) const {
+    if constexpr (VEC) {
+      const int c = (l + j * R) * 8;
+      if (c < d) {
+        uint4* p = reinterpret_cast<uint4*>(row + c);
+        const uint4* q = reinterpret_cast<const uint4*>(v);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) p[i] = q[i];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = l + R * (j * 8 + e);
+        if (c < d) row[c] = v[e];
+      }
+    }
+  }
+};
+
+// Column of element e of group j (VEC: 8 neighbours; else R apart).
+template <bool VEC>
+__device__ __forceinline__ int column(int l, int j, int e, int R) {
+  return VEC ? (l + j * R) * 8 + e : l + R * (j * 8 + e);
+}
+
+template <bool VEC, int NV>
+__device__ __forceinline__ void load_params(const float* p, float fill, int l, int R, int d,
+                                            float (&out)[NV][8]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = column<VEC>(l, j, e, R);
+      out[j][e] = c >= d ? 0.f : p != nullptr ? __ldg(p + c) : fill;
+    }
+}
+
+// Sums of K values over the R threads of a row (R <= 32: within the warp; R
+// > 32: the whole block, one barrier, two buffers in turn).  The order of
+// the additions is fixed.
+template <int R, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], float* buf, int& phase) {
+#pragma unroll
+  for (int m = (R < 32 ? R : 32) / 2; m > 0; m >>= 1)
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], m);
+  if constexpr (R > 32) {
+    constexpr int W = R / 32;
+    float* b = buf + phase * 2 * W;
+    phase ^= 1;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) b[i * W + (threadIdx.x >> 5)] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += b[i * W + w];
+      v[i] = s;
+    }
+  }
+}
+
+// act(z) and act'(z).  kind 0: z, 1: sigmoid(z), 2: z sigmoid(z).
+__device__ __forceinline__ float gate_value(float z, int kind) {
+  if (kind == 0) return z;
+  const float s = __fdividef(1.f, 1.f + __expf(-z));
+  return kind == 1 ? s : z * s;
+}
+__device__ __forceinline__ float gate_slope(float z, int kind, float& a) {
+  if (kind == 0) {
+    a = z;
+    return 1.f;
+  }
+  const float s = __fdividef(1.f, 1.f + __expf(-z));
+  if (kind == 1) {
+    a = s;
+    return s * (1.f - s);
+  }
+  a = z * s;
+  return s * (1.f + z * (1.f - s));
+}
+
+// In place: v -> (v - mean) with mean the row's (layer form); returns rstd.
+template <bool VEC, int R, int NV>
+__device__ __forceinline__ float centre(float (&v)[NV][8], const NormArgs& a, int l, float* buf,
+                                        int& phase) {
+  if (a.layer) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[0] += v[j][e];
+    row_sum<R, 1>(s, buf, phase);
+    const float mean = s[0] * a.inv_d;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[j][e] = column<VEC>(l, j, e, R) < a.d ? v[j][e] - mean : 0.f;
+  }
+  float q[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[0] = fmaf(v[j][e], v[j][e], q[0]);
+  row_sum<R, 1>(q, buf, phase);
+  return rsqrtf(fmaf(q[0], a.inv_d, a.eps));
+}
+
+template <int R>
+__host__ __device__ constexpr int norm_threads() { return R <= 256 ? (R <= 128 ? 128 : 256) : R; }
+
+template <class TB, class TR, int R, int NV, bool VEC>
+__global__ void __launch_bounds__(norm_threads<R>())
+    block_norm_forward_kernel(const NormArgs a) {
+  constexpr int T = norm_threads<R>();
+  constexpr int G = R > 32 ? 1 : T / R;  // rows per block (R > 32: R == T)
+  static_assert(R <= 32 || R == T, "one row per block above a warp");
+  __shared__ float buf[4 * (T / 32)];
+  const int l = R > 32 ? threadIdx.x : threadIdx.x % R;
+  const int grp = R > 32 ? 0 : threadIdx.x / R;
+  int phase = 0;
+  float g1[NV][8], b1[NV][8], rs[NV][8], g2[NV][8], b2[NV][8];
+  load_params<VEC, NV>(a.g1, 1.f, l, R, a.d, g1);
+  load_params<VEC, NV>(a.b1, 0.f, l, R, a.d, b1);
+  load_params<VEC, NV>(a.rs, 1.f, l, R, a.d, rs);
+  load_params<VEC, NV>(a.g2, 1.f, l, R, a.d, g2);
+  load_params<VEC, NV>(a.b2, 0.f, l, R, a.d, b2);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  Frag<TR, VEC> fx[NV];
+  Frag<TB, VEC> fy[NV], fz[NV];
+  auto fetch = [&](int64_t row) {
+    if (row >= a.rows) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      fx[j].load(static_cast<const TR*>(a.x) + row * a.ldx, l, j, R, a.d);
+      if (a.y != nullptr) fy[j].load(static_cast<const TB*>(a.y) + row * a.ldy, l, j, R, a.d);
+      if (a.z != nullptr) fz[j].load(static_cast<const TB*>(a.z) + row * a.ldz, l, j, R, a.d);
+    }
+  };
+  // Groups past the last row go through the same reductions on old values
+  // and store nothing.
+  fetch(static_cast<int64_t>(blockIdx.x) * G + grp);
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < a.rows; row0 += step) {
+    const int64_t row = row0 + grp;
+    const bool live = row < a.rows;
+    float x[NV][8], y[NV][8], z[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[j][e] = to_f(fx[j].v[e]);
+        y[j][e] = a.y != nullptr ? to_f(fy[j].v[e]) : 0.f;
+        z[j][e] = a.z != nullptr ? to_f(fz[j].v[e]) : 0.f;
+      }
+    fetch(row + step);
+    if (a.y != nullptr) {
+      const float ry = a.g1 != nullptr ? centre<VEC, R, NV>(y, a, l, buf, phase) : 1.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float n = fmaf(y[j][e] * ry, g1[j][e], b1[j][e]);
+          const float act = a.z != nullptr ? gate_value(z[j][e], a.gate_kind) : 1.f;
+          x[j][e] = fmaf(rs[j][e] * act, n, x[j][e]);
+        }
+      if (a.o1 != nullptr && live) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          Frag<TR, VEC> o;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) from_f(x[j][e], o.v[e]);
+          o.store(static_cast<TR*>(a.o1) + row * a.d, l, j, R, a.d);
+        }
+      }
+    }
+    if (a.o2 != nullptr) {
+      const float rr = centre<VEC, R, NV>(x, a, l, buf, phase);
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          Frag<TB, VEC> o;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) from_f(fmaf(x[j][e] * rr, g2[j][e], b2[j][e]), o.v[e]);
+          o.store(static_cast<TB*>(a.o2) + row * a.d, l, j, R, a.d);
+        }
+      }
+    }
+  }
+}
+
+template <class TB, class TR, int R, int NV, bool VEC>
+__global__ void __launch_bounds__(norm_threads<R>())
+    block_norm_backward_kernel(const NormArgs a) {
+  constexpr int T = norm_threads<R>();
+  constexpr int G = R > 32 ? 1 : T / R;
+  static_assert(R <= 32 || R == T, "one row per block above a warp");
+  __shared__ float buf[4 * (T / 32)];
+  __shared__ float red[G > 1 ? T * 8 : 1];
+  const int l = R > 32 ? threadIdx.x : threadIdx.x % R;
+  const int grp = R > 32 ? 0 : threadIdx.x / R;
+  int phase = 0;
+  float g1[NV][8], b1[NV][8], rs[NV][8], g2[NV][8];
+  load_params<VEC, NV>(a.g1, 1.f, l, R, a.d, g1);
+  load_params<VEC, NV>(a.b1, 0.f, l, R, a.d, b1);
+  load_params<VEC, NV>(a.rs, 1.f, l, R, a.d, rs);
+  load_params<VEC, NV>(a.g2, 1.f, l, R, a.d, g2);
+  float acc[5][NV][8];  // dg1, db1, drs, dg2, db2
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[i][j][e] = 0.f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  Frag<TR, VEC> fx[NV], fdr[NV];
+  Frag<TB, VEC> fy[NV], fz[NV], fdu[NV];
+  auto fetch = [&](int64_t row) {
+    if (row >= a.rows) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (a.du != nullptr) {
+        fx[j].load(static_cast<const TR*>(a.x) + row * a.ldx, l, j, R, a.d);
+        fdu[j].load(static_cast<const TB*>(a.du) + row * a.lddu, l, j, R, a.d);
+      }
+      if (a.y != nullptr) fy[j].load(static_cast<const TB*>(a.y) + row * a.ldy, l, j, R, a.d);
+      if (a.z != nullptr) fz[j].load(static_cast<const TB*>(a.z) + row * a.ldz, l, j, R, a.d);
+      if (a.dr != nullptr) fdr[j].load(static_cast<const TR*>(a.dr) + row * a.lddr, l, j, R, a.d);
+    }
+  };
+  fetch(static_cast<int64_t>(blockIdx.x) * G + grp);
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < a.rows; row0 += step) {
+    const int64_t row = row0 + grp;
+    const bool live = row < a.rows;
+    float x[NV][8], dx[NV][8], y[NV][8], z[NV][8], h[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[j][e] = a.du != nullptr ? to_f(fx[j].v[e]) : 0.f;
+        h[j][e] = live && a.du != nullptr ? to_f(fdu[j].v[e]) : 0.f;
+        y[j][e] = a.y != nullptr ? to_f(fy[j].v[e]) : 0.f;
+        z[j][e] = a.z != nullptr ? to_f(fz[j].v[e]) : 0.f;
+        dx[j][e] = live && a.dr != nullptr ? to_f(fdr[j].v[e]) : 0.f;
+      }
+    fetch(row + step);
+    if (a.du != nullptr) {
+      const float rr = centre<VEC, R, NV>(x, a, l, buf, phase);
+      float s[2] = {0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float xh = x[j][e] * rr, du = h[j][e];
+          if (live) {
+            acc[3][j][e] = fmaf(du, xh, acc[3][j][e]);
+            acc[4][j][e] += du;
+          }
+          x[j][e] = xh;
+          h[j][e] = du * g2[j][e];
+          s[0] = fmaf(h[j][e], xh, s[0]);
+          s[1] += h[j][e];
+        }
+      row_sum<R, 2>(s, buf, phase);
+      const float c1 = s[0] * a.inv_d, c2 = a.layer ? s[1] * a.inv_d : 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dx[j][e] = fmaf(rr, h[j][e] - c2 - x[j][e] * c1, dx[j][e]);
+    }
+    if (a.o1 != nullptr && live) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        Frag<TR, VEC> o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) from_f(dx[j][e], o.v[e]);
+        o.store(static_cast<TR*>(a.o1) + row * a.d, l, j, R, a.d);
+      }
+    }
+    if (a.y != nullptr) {
+      const float ry = a.g1 != nullptr ? centre<VEC, R, NV>(y, a, l, buf, phase) : 1.f;
+      float s[2] = {0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float yh = y[j][e] * ry;
+          const float n = fmaf(yh, g1[j][e], b1[j][e]);
+          float act = 1.f, slope = 0.f;
+          if (a.z != nullptr) slope = gate_slope(z[j][e], a.gate_kind, act);
+          const float ds = dx[j][e] * rs[j][e];
+          const float dn = ds * act;
+          z[j][e] = ds * n * slope;  // dz
+          if (live) {
+            acc[2][j][e] = fmaf(dx[j][e] * act, n, acc[2][j][e]);
+            acc[0][j][e] = fmaf(dn, yh, acc[0][j][e]);
+            acc[1][j][e] += dn;
+          }
+          const float p = dn * g1[j][e];
+          y[j][e] = yh;
+          dx[j][e] = p;
+          s[0] = fmaf(p, yh, s[0]);
+          s[1] += p;
+        }
+      if (a.o3 != nullptr && live) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          Frag<TB, VEC> o;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) from_f(z[j][e], o.v[e]);
+          o.store(static_cast<TB*>(a.o3) + row * a.d, l, j, R, a.d);
+        }
+      }
+      if (a.g1 != nullptr) {
+        row_sum<R, 2>(s, buf, phase);
+        const float c1 = s[0] * a.inv_d, c2 = a.layer ? s[1] * a.inv_d : 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dx[j][e] = ry * (dx[j][e] - c2 - y[j][e] * c1);
+      }
+      if (a.o2 != nullptr && live) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          Frag<TB, VEC> o;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) from_f(dx[j][e], o.v[e]);
+          o.store(static_cast<TB*>(a.o2) + row * a.d, l, j, R, a.d);
+        }
+      }
+    }
+  }
+  if (!a.sums) return;
+  // The block's column sums: its row groups in ascending order.
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 5 * a.d;
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (G > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) red[e * T + threadIdx.x] = acc[i][j][e];
+        __syncthreads();
+        if (grp == 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float s = 0.f;
+            for (int g = 0; g < G; ++g) s += red[e * T + g * R + l];
+            const int c = column<VEC>(l, j, e, R);
+            if (c < a.d) part[i * a.d + c] = s;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = column<VEC>(l, j, e, R);
+          if (c < a.d) part[i * a.d + c] = acc[i][j][e];
+        }
+      }
+    }
+}
+
+struct NormSums {
+  float* out[5];
+};
+
+// out[i][c] = the blocks' column sums in ascending order (8 interleaved runs
+// per column in fp64, joined in a fixed order): bitwise reproducible.
+__global__ void __launch_bounds__(256) block_norm_sums_kernel(const float* part, int blocks, int d,
+                                                              NormSums o) {
+  __shared__ double red[8][32];
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane, n = 5 * d;
+  grid_dependency_wait();
+  double s = 0.0;
+  if (e < n)
+    for (int b = run; b < blocks; b += 8) s += part[static_cast<int64_t>(b) * n + e];
+  red[run][lane] = s;
+  __syncthreads();
+  if (run == 0 && e < n) {
+    for (int r = 1; r < 8; ++r) s += red[r][lane];
+    float* out = o.out[e / d];
+    if (out != nullptr) out[e % d] = static_cast<float>(s);
+  }
+}
+
+// Threads per row: the power of two that covers d with one group of 8
+// columns per thread, 4 to 512; above 4096 columns two groups.
+int row_threads(int d) {
+  int r = 4;
+  while (r * 8 < d && r < 512) r *= 2;
+  return r == 64 ? 128 : r;  // a block of one row has at least 128 threads
+}
+
+template <class TB, class TR, int R, int NV, bool VEC>
+cudaError_t launch_norm(const NormArgs& a, bool backward, int sms, int* blocks, cudaStream_t st) {
+  constexpr int T = norm_threads<R>();
+  constexpr int G = R > 32 ? 1 : T / R;
+  auto kernel = backward ? block_norm_backward_kernel<TB, TR, R, NV, VEC>
+                         : block_norm_forward_kernel<TB, TR, R, NV, VEC>;
+  int per_sm = 0;
+  cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, T, 0);
+  if (err != cudaSuccess) return err;
+  const int64_t need = (a.rows + G - 1) / G;
+  const int64_t most = static_cast<int64_t>(sms) * (per_sm < 1 ? 1 : per_sm);
+  *blocks = static_cast<int>(need < most ? need : most);
+  kernel<<<static_cast<unsigned>(*blocks), T, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <class TB, class TR, bool VEC>
+cudaError_t dispatch_width(const NormArgs& a, bool backward, int sms, int* blocks,
+                           cudaStream_t st) {
+  switch (row_threads(a.d)) {
+    case 4: return launch_norm<TB, TR, 4, 1, VEC>(a, backward, sms, blocks, st);
+    case 8: return launch_norm<TB, TR, 8, 1, VEC>(a, backward, sms, blocks, st);
+    case 16: return launch_norm<TB, TR, 16, 1, VEC>(a, backward, sms, blocks, st);
+    case 32: return launch_norm<TB, TR, 32, 1, VEC>(a, backward, sms, blocks, st);
+    case 128: return launch_norm<TB, TR, 128, 1, VEC>(a, backward, sms, blocks, st);
+    case 256: return launch_norm<TB, TR, 256, 1, VEC>(a, backward, sms, blocks, st);
+    default:
+      return a.d <= 4096 ? launch_norm<TB, TR, 512, 1, VEC>(a, backward, sms, blocks, st)
+                         : launch_norm<TB, TR, 512, kMaxNormRows, VEC>(a, backward, sms, blocks, st);
+  }
+}
+
+bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// 16-byte accesses: every row of every operand starts on a 16-byte boundary
+// and holds whole groups of 8 columns.
+bool vector_rows(const NormArgs& a, size_t er, size_t eb) {
+  if (a.d % 8 != 0) return false;
+  const void* rp[] = {a.x, a.dr, a.o1};
+  const int64_t rl[] = {a.x ? a.ldx : 0, a.dr ? a.lddr : 0, 0};
+  for (int i = 0; i < 3; ++i)
+    if (!al(rp[i], 16) || rl[i] * er % 16 != 0) return false;
+  const void* bp[] = {a.y, a.z, a.du, a.o2, a.o3};
+  const int64_t bl[] = {a.y ? a.ldy : 0, a.z ? a.ldz : 0, a.du ? a.lddu : 0, 0, 0};
+  for (int i = 0; i < 5; ++i)
+    if (!al(bp[i], 16) || bl[i] * eb % 16 != 0) return false;
+  return true;
+}
+
+cudaError_t dispatch(const NormArgs& a, sa_dtype tr, sa_dtype tb, bool backward, int sms,
+                     int* blocks, cudaStream_t st) {
+  const bool vec = vector_rows(a, tr == SA_BF16 ? 2 : 4, tb == SA_BF16 ? 2 : 4);
+  if (tb == SA_FP32)
+    return vec ? dispatch_width<float, float, true>(a, backward, sms, blocks, st)
+               : dispatch_width<float, float, false>(a, backward, sms, blocks, st);
+  if (tr == SA_FP32)
+    return vec ? dispatch_width<uint16_t, float, true>(a, backward, sms, blocks, st)
+               : dispatch_width<uint16_t, float, false>(a, backward, sms, blocks, st);
+  return vec ? dispatch_width<uint16_t, uint16_t, true>(a, backward, sms, blocks, st)
+             : dispatch_width<uint16_t, uint16_t, false>(a, backward, sms, blocks, st);
+}
+
+// Most blocks the backward pass may launch on a device of `sms` SMs (its
+// partial sums are sized for them): 16 blocks of 128 threads fill an SM.
+int64_t most_blocks(int sms, int d) {
+  const int r = row_threads(d);
+  const int t = r <= 128 ? 128 : r;
+  return static_cast<int64_t>(sms) * (2048 / t);
+}
+
+sa_status device_sms(int* sms) {
+  int dev = 0, major = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SA_ERR_CUDA;
+  return major == 10 ? SA_OK : SA_ERR_UNSUPPORTED;
+}
+
+bool norm_args_ok(const NormArgs& a, sa_dtype tr, sa_dtype tb, int kind, int gate_kind) {
+  if (a.rows < 0 || a.rows >= (int64_t{1} << 40) || a.d < 1 || a.d > kMaxNormWidth) return false;
+  if ((tr != SA_BF16 && tr != SA_FP32) || (tb != SA_BF16 && tb != SA_FP32) ||
+      (tb == SA_FP32 && tr != SA_FP32))
+    return false;
+  if (kind < 0 || kind > 1 || gate_kind < 0 || gate_kind > 2) return false;
+  if (!(a.eps > 0.f) || !(a.eps < 3.0e38f)) return false;
+  const size_t er = tr == SA_BF16 ? 2 : 4, eb = tb == SA_BF16 ? 2 : 4;
+  if (!al(a.x, er) || !al(a.y, eb) || !al(a.z, eb) || !al(a.dr, er) || !al(a.du, eb) ||
+      !al(a.o1, er) || !al(a.g1, 4) || !al(a.b1, 4) || !al(a.rs, 4) || !al(a.g2, 4) ||
+      !al(a.b2, 4) || !al(a.o2, eb) || !al(a.o3, eb))
+    return false;
+  const int64_t ld[] = {a.ldx, a.y ? a.ldy : a.d, a.z ? a.ldz : a.d, a.dr ? a.lddr : a.d,
+                        a.du ? a.lddu : a.d};
+  for (int64_t l : ld)
+    if (l < a.d || l >= (int64_t{1} << 40)) return false;
+  // What applies to the block's output needs a block, a bias its gain.
+  if (a.y == nullptr && (a.z || a.g1 || a.rs)) return false;
+  if ((a.b1 && !a.g1) || (a.b2 && !a.g2)) return false;
+  return true;
+}
+
+}  // namespace
+}  // namespace sa
+
+extern "C" {
+
+sa_status sa_block_norm_forward(const void* residual, int64_t ld_residual, const void* block,
+                                int64_t ld_block, const void* gate, int64_t ld_gate,
+                                const float* post_gain, const float* post_bias,
+                                const float* res_scale, const float* pre_gain,
+                                const float* pre_bias, int64_t rows, int d,
+                                sa_dtype residual_dtype, sa_dtype dtype, sa_norm_kind kind,
+                                sa_gate_kind gate_kind, float eps, void* residual_out,
+                                void* normed, void* stream) {
+  sa::NormArgs a = {};
+  a.x = residual, a.y = block, a.z = gate;
+  a.ldx = ld_residual, a.ldy = ld_block, a.ldz = ld_gate;
+  a.g1 = post_gain, a.b1 = post_bias, a.rs = res_scale, a.g2 = pre_gain, a.b2 = pre_bias;
+  a.o1 = residual_out, a.o2 = normed;
+  a.rows = rows, a.d = d, a.layer = kind == SA_NORM_LAYER, a.gate_kind = gate_kind;
+  a.eps = eps, a.inv_d = d > 0 ? 1.f / static_cast<float>(d) : 0.f;
+  if (!sa::norm_args_ok(a, residual_dtype, dtype, kind, gate_kind)) return SA_ERR_INVALID_ARG;
+  // u needs its gain; r is written if and only if there is a block to add.
+  if ((normed == nullptr) != (pre_gain == nullptr) || (residual_out == nullptr) != (block == nullptr) ||
+      (normed == nullptr && residual_out == nullptr))
+    return SA_ERR_INVALID_ARG;
+  if (rows == 0) return SA_OK;
+  if (residual == nullptr) return SA_ERR_INVALID_ARG;
+  int sms = 0, blocks = 0;
+  const sa_status s = sa::device_sms(&sms);
+  if (s != SA_OK) return s;
+  return sa::dispatch(a, residual_dtype, dtype, false, sms, &blocks,
+                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SA_OK
+             : SA_ERR_CUDA;
+}
+
+size_t sa_workspace_bytes_block_norm(int64_t rows, int d) {
+  int sms = 0;
+  if (rows < 0 || d < 1 || d > sa::kMaxNormWidth || sa::device_sms(&sms) != SA_OK) return 0;
+  const int64_t most = sa::most_blocks(sms, d);
+  const int64_t blocks = rows < 1 ? 1 : rows < most ? rows : most;
+  return static_cast<size_t>(blocks) * 5 * d * sizeof(float);
+}
+
+sa_status sa_block_norm_backward(const void* residual_out, int64_t ld_residual, const void* block,
+                                 int64_t ld_block, const void* gate, int64_t ld_gate,
+                                 const float* post_gain, const float* post_bias,
+                                 const float* res_scale, const float* pre_gain, int64_t rows,
+                                 int d, sa_dtype residual_dtype, sa_dtype dtype,
+                                 sa_norm_kind kind, sa_gate_kind gate_kind, float eps,
+                                 const void* d_residual_out, int64_t ld_d_residual,
+                                 const void* d_normed, int64_t ld_d_normed, void* d_residual,
+                                 void* d_block, void* d_gate, float* d_post_gain,
+                                 float* d_post_bias, float* d_res_scale, float* d_pre_gain,
+                                 float* d_pre_bias, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  sa::NormArgs a = {};
+  a.x = residual_out, a.y = block, a.z = gate;
+  a.ldx = d_normed != nullptr ? ld_residual : d, a.ldy = ld_block, a.ldz = ld_gate;
+  a.g1 = post_gain, a.b1 = post_bias, a.rs = res_scale, a.g2 = pre_gain;
+  a.dr = d_residual_out, a.du = d_normed, a.lddr = ld_d_residual, a.lddu = ld_d_normed;
+  a.o1 = d_residual, a.o2 = d_block, a.o3 = d_gate;
+  a.rows = rows, a.d = d, a.layer = kind == SA_NORM_LAYER, a.gate_kind = gate_kind;
+  a.eps = eps, a.inv_d = d > 0 ? 1.f / static_cast<float>(d) : 0.f;
+  a.part = static_cast<float*>(workspace);
+  const sa::NormSums sums = {{d_post_gain, d_post_bias, d_res_scale, d_pre_gain, d_pre_bias}};
+  for (float* p : sums.out) {
+    if (!sa::al(p, 4)) return SA_ERR_INVALID_ARG;
+    a.sums |= p != nullptr;
+  }
+  if (!sa::norm_args_ok(a, residual_dtype, dtype, kind, gate_kind)) return SA_ERR_INVALID_ARG;
+  if ((d_normed == nullptr) != (pre_gain == nullptr) ||
+      (d_normed == nullptr && d_residual_out == nullptr) || d_residual == nullptr ||
+      (block == nullptr) != (d_block == nullptr) || (gate == nullptr) != (d_gate == nullptr) ||
+      ((d_post_gain || d_post_bias) && !post_gain) || (d_res_scale && !block) ||
+      ((d_pre_gain || d_pre_bias) && !pre_gain))
+    return SA_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    for (float* p : sums.out)
+      if (p != nullptr && cudaMemsetAsync(p, 0, sizeof(float) * d, st) != cudaSuccess)
+        return SA_ERR_CUDA;
+    return SA_OK;
+  }
+  if (d_normed != nullptr && residual_out == nullptr) return SA_ERR_INVALID_ARG;
+  int sms = 0, blocks = 0;
+  const sa_status s = sa::device_sms(&sms);
+  if (s != SA_OK) return s;
+  if (a.sums) {
+    if (workspace == nullptr || !sa::al(workspace, 16)) return SA_ERR_INVALID_ARG;
+    if (workspace_bytes < sa_workspace_bytes_block_norm(rows, d)) return SA_ERR_WORKSPACE;
+  }
+  if (sa::dispatch(a, residual_dtype, dtype, true, sms, &blocks, st) != cudaSuccess)
+    return SA_ERR_CUDA;
+  if (!a.sums) return SA_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((5 * d + 31) / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sa::block_norm_sums_kernel,
+                            static_cast<const float*>(workspace), blocks, d, sums) == cudaSuccess
+             ? SA_OK
+             : SA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,470 @@
+// Linear attention with a decay per head: the C entry points, the CUDA-core
+// scan and the single-step kernel.  The formulas are in sa_linear_attention.h.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "sa.h"
+#include "sa_internal.h"
+#include "sa_linear_attention.h"
+#include "sa_ptx.cuh"
+
+namespace sa {
+namespace {
+
+__device__ __forceinline__ float load_f(const float* p) { return *p; }
+__device__ __forceinline__ float load_f(const uint16_t* p) {
+  return __uint_as_float(static_cast<uint32_t>(*p) << 16);
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = v[i];
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+}
+
+// ---------------------------------------------------------------- states between segments
+// Boundary j receives the state (gradient of the state) behind (before) it,
+// from the segments' own sums.  One thread per four state elements, segment
+// after segment, the next ones' sums loaded ahead.
+struct ChainArgs {
+  int reverse;
+  const float* ends;
+  float ends_mul;
+  float* bound;
+};
+
+__global__ void __launch_bounds__(256)
+    state_chain_kernel(const ScanCommon s, int64_t segment, int elems, const ChainArgs f,
+                       const ChainArgs r) {
+  const ChainArgs& a = blockIdx.z == 0 ? f : r;
+  const int64_t b = blockIdx.x / s.heads;
+  const int head = static_cast<int>(blockIdx.x % s.heads);
+  int64_t lo, hi;
+  user_rows(s, b, lo, hi);
+  const int64_t n = hi - lo, count = n > 0 ? (n + segment - 1) / segment : 1;
+  const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (count < 2 || e >= elems) return;
+  const double g = static_cast<double>(usable_decay(s.log_decay[head]));
+  const int64_t step = static_cast<int64_t>(s.heads) * elems;
+  float* p = a.bound + ((lo / segment) * s.heads + head) * static_cast<int64_t>(elems) + e;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.ends != nullptr) {
+    v = *reinterpret_cast<const float4*>(a.ends + (b * s.heads + head) * static_cast<int64_t>(elems) + e);
+    v.x *= a.ends_mul, v.y *= a.ends_mul, v.z *= a.ends_mul, v.w *= a.ends_mul;
+  }
+  const float whole = static_cast<float>(exp(g * static_cast<double>(segment)));
+  const int64_t tail = n - (count - 1) * segment - 1;  // the last segment's rows but one
+  const float first = a.reverse ? static_cast<float>(exp(g * static_cast<double>(tail))) : whole;
+  constexpr int kAhead = 4;
+  float4 x[kAhead];
+  auto at = [&](int64_t j) {
+    return reinterpret_cast<float4*>(p + (a.reverse ? count - 2 - j : j) * step);
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (k < count - 1) x[k] = *at(k);
+  for (int64_t j = 0; j < count - 1; j += kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (j + k >= count - 1) break;
+      const float m = j + k == 0 ? first : whole;
+      v.x = fmaf(m, v.x, x[k].x);
+      v.y = fmaf(m, v.y, x[k].y);
+      v.z = fmaf(m, v.z, x[k].z);
+      v.w = fmaf(m, v.w, x[k].w);
+      if (j + k + kAhead < count - 1) x[k] = *at(j + k + kAhead);
+      *at(j + k) = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- one step
+// S <- l S + k v^T, o = mul S^T q for one row of each listed state.  Bound
+// by reading and writing the state once: a thread takes four columns of
+// every (threads / column groups)-th state row, its loads issued in batches
+// before they are used, and the partial outputs are joined in shared memory
+// in a fixed order.
+struct StepArgs {
+  ScanInput q, k, v;       // strides: row = batch entry
+  const float* log_decay;
+  const int64_t* slots;    // may be null: entry b uses state b
+  int64_t batch, states;
+  float* state;            // [states][H][dk][dv]
+  void* out;               // [batch][H][dv]
+  int heads, dk, dv;
+  int cols4;               // four-column groups per block
+  float mul;
+  uint32_t* flags;         // may be null
+};
+
+constexpr int kStepThreads = 256, kStepBatch = 8, kStepMaxWidth = 256;
+
+template <class T>
+__global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
+  __shared__ float sq[kStepMaxWidth], sk[kStepMaxWidth];
+  __shared__ float4 red[kStepThreads];
+  const int tid = threadIdx.x;
+  const int64_t b = blockIdx.x / a.heads;
+  const int h = static_cast<int>(blockIdx.x % a.heads);
+  const int groups = kStepThreads / a.cols4;         // state rows taken at a time
+  const int c4 = tid % a.cols4, g = tid / a.cols4;
+  const int col = (blockIdx.y * a.cols4 + c4) * 4;   // first column
+  const bool live = g < groups && col < a.dv;
+  int64_t slot = b;
+  if (a.slots != nullptr) {
+    // A negative slot marks a padded entry.  Of entries with equal slots the
+    // first is taken; a later one, or a slot past the pool, raises the flag.
+    slot = a.slots[b];
+    bool twice = false;
+    if (slot >= 0)
+      for (int64_t i = tid; i < b; i += kStepThreads) twice |= a.slots[i] == slot;
+    if (__syncthreads_or(twice) || slot >= a.states) {
+      if (tid == 0 && a.flags != nullptr) atomicOr(a.flags, SA_DEVFLAG_SLOT);
+      slot = -1;
+    }
+  }
+  T* out = static_cast<T*>(a.out) + (b * a.heads + h) * a.dv + col;
+  if (slot < 0) {
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    if (g == 0 && col < a.dv) store4(out, zero);
+    return;
+  }
+  const float gd = a.log_decay[h];
+  if (!(gd <= 0.f) && tid == 0 && a.flags != nullptr) atomicOr(a.flags, SA_DEVFLAG_DECAY);
+  const float l = expf(usable_decay(gd));
+  float* st = a.state + ((slot * a.heads + h) * a.dk) * a.dv + col;
+  const T* vp = static_cast<const T*>(a.v.p) + b * a.v.row + h * a.v.head + col;
+  float v[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+  float4 s[kStepBatch];
+  auto fetch = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kStepBatch; ++i) {
+      const int r = r0 + i * groups;
+      if (live && r < a.dk) s[i] = *reinterpret_cast<const float4*>(st + static_cast<int64_t>(r) * a.dv);
+    }
+  };
+  fetch(g);
+  for (int i = tid; i < a.dk; i += kStepThreads) {
+    sq[i] = load_f(static_cast<const T*>(a.q.p) + b * a.q.row + h * a.q.head + i);
+    sk[i] = load_f(static_cast<const T*>(a.k.p) + b * a.k.row + h * a.k.head + i);
+  }
+  if (live) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = load_f(vp + c);
+  }
+  __syncthreads();
+  for (int r0 = g; r0 < a.dk; r0 += kStepBatch * groups) {
+    if (r0 != g) fetch(r0);
+#pragma unroll
+    for (int i = 0; i < kStepBatch; ++i) {
+      const int r = r0 + i * groups;
+      if (!live || r >= a.dk) continue;
+      const float kv = sk[r], qv = sq[r];
+      float4 x = s[i];
+      x.x = fmaf(kv, v[0], l * x.x);
+      x.y = fmaf(kv, v[1], l * x.y);
+      x.z = fmaf(kv, v[2], l * x.z);
+      x.w = fmaf(kv, v[3], l * x.w);
+      *reinterpret_cast<float4*>(st + static_cast<int64_t>(r) * a.dv) = x;
+      o[0] = fmaf(qv, x.x, o[0]);
+      o[1] = fmaf(qv, x.y, o[1]);
+      o[2] = fmaf(qv, x.z, o[2]);
+      o[3] = fmaf(qv, x.w, o[3]);
+    }
+  }
+  red[tid] = make_float4(o[0], o[1], o[2], o[3]);
+  __syncthreads();
+  if (g == 0 && col < a.dv) {
+    for (int i = 1; i < groups; ++i) {
+      const float4 x = red[i * a.cols4 + c4];
+      o[0] += x.x;
+      o[1] += x.y;
+      o[2] += x.z;
+      o[3] += x.w;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] *= a.mul;
+    store4(out, o);
+  }
+}
+
+bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+bool width_ok(int d) { return d == 64 || d == 128; }
+
+bool input_ok(const ScanInput& in, int heads, int d, size_t elem) {
+  const int64_t most = int64_t{1} << 40;
+  return al(in.p, elem) && in.row >= 0 && in.row < most && in.head >= 0 && in.head < most &&
+         (heads == 1 || in.head >= d);
+}
+
+bool common_ok(const ScanCommon& s, int dk, int dv, sa_dtype dtype, float scale) {
+  return s.batch >= 0 && s.batch < (int64_t{1} << 31) / 1024 && s.rows >= 0 &&
+         s.rows < (int64_t{1} << 31) - 256 && s.heads >= 1 && s.heads <= 1024 && width_ok(dk) &&
+         width_ok(dv) && (dtype == SA_BF16 || dtype == SA_FP32) && isfinite(scale) &&
+         fabsf(scale) >= 1e-20f && fabsf(scale) <= 1e20f && s.log_decay != nullptr &&
+         s.offsets != nullptr && al(s.log_decay, 4) && al(s.offsets, 8);
+}
+
+sa_status on_sm100() {
+  int dev = 0, major = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+    return SA_ERR_CUDA;
+  return major == 10 ? SA_OK : SA_ERR_UNSUPPORTED;
+}
+
+// Rows per segment, or 0 where histories stay whole, for `scans` scans of the
+// batch.  In rows of one head on one SM: whole, they take their share of all
+// rows or the longest history (equal histories in rounds, unequal ones end
+// with the longest), whichever is more; split, the share, the states' sums
+// (about half as much again), one segment and the extra launches.  Four
+// segments per SM even out the segments' ends.
+struct SplitRule {
+  int64_t tile, least, launches;  // rows: chunk, shortest segment, the extra launches' worth
+};
+constexpr SplitRule kSplitSimt = {64, 64, 32};
+
+int64_t split_rows(const SplitRule& rule, int64_t batch, int64_t rows, int64_t max_rows, int heads,
+                   int scans, int sms) {
+  const int64_t longest = max_rows > 0 && max_rows < rows ? max_rows : rows;
+  const int64_t share = rows * heads * scans / sms;
+  int64_t segment = (share / 4 + rule.tile - 1) / rule.tile * rule.tile;
+  if (segment < rule.least) segment = rule.least;
+  if (longest < 2 * segment) return 0;
+  const int64_t waves = (batch * heads * scans + sms - 1) / sms;
+  int64_t whole = share > longest ? share : longest;
+  if (batch * longest <= rows + rows / 8 && waves * longest > whole) whole = waves * longest;
+  return whole > share + share / 2 + segment + rule.launches ? segment : 0;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// The states between segments, one direction.
+size_t bound_bytes(int64_t rows, int64_t segment, int heads, int elems) {
+  return segment == 0 ? 0 : up256(static_cast<size_t>(rows / segment) * heads * elems * 4);
+}
+
+size_t state_bytes(int64_t batch, int heads, int elems) {
+  return up256(static_cast<size_t>(batch) * heads * elems * 4);
+}
+
+int device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// Runs n scans (n = 1: the forward; n = 3: dq, dk, dv) of one batch.  The
+// workspace: header | states between segments, forward, reverse | a copy of
+// the initial states (forward scans whose final states replace them).
+cudaError_t run_scans(ScanPass* passes, int n, const ScanCommon& s, int64_t max_rows, int d_k,
+                      int d_v, bool bf16, int sms, cudaStream_t st) {
+  const int elems = d_k * d_v;
+  const int64_t segment = split_rows(kSplitSimt, s.batch, s.rows, max_rows, s.heads, n, sms);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(s.header) + kWsHeaderBytes;
+  const size_t half = bound_bytes(s.rows, segment, s.heads, elems);
+  for (int i = 0; i < n; ++i) passes[i].bound = reinterpret_cast<float*>(ws + passes[i].reverse * half);
+  ScanArgs t = {};
+  t.s = s;
+  t.check = 1;
+  t.segment = segment == 0 ? s.rows + 1 : segment;
+  const int64_t slots = s.batch + (segment == 0 ? 0 : s.rows / segment);
+  cudaError_t err = cudaSuccess;
+  if (segment != 0) {
+    if (n == 1 && passes[0].ends != nullptr && passes[0].ends == passes[0].fin) {
+      // The last segment's final state must not meet the first one's start.
+      void* copy = ws + 2 * half;
+      err = cudaMemcpyAsync(copy, passes[0].ends, static_cast<size_t>(s.batch) * s.heads * elems * 4,
+                            cudaMemcpyDeviceToDevice, st);
+      passes[0].ends = static_cast<const float*>(copy);
+    }
+    // The states of the forward direction are sums over k and v, those of
+    // the reverse one over q and d_out (dv's b and c), each stored once.
+    ScanArgs u = t;
+    ChainArgs chain[2] = {};
+    for (int i = 0; i < n; ++i) {
+      const ScanPass& p = passes[i];
+      if (n == 3 && i == 1) continue;  // dk shares dv's
+      ScanPass& o = u.p[u.passes++] = p;
+      if (n == 3 && i == 0) {          // dq's (a, b, c) = (do, v, k)
+        o.b = p.c, o.c = p.b;
+        o.map_b = p.map_c, o.map_c = p.map_b;
+      }
+      o.da = d_k, o.dc = d_v;
+      chain[p.reverse] = {p.reverse, p.ends, p.ends_mul, p.bound};
+    }
+    u.items = slots * s.heads * u.passes;
+    if (err == cudaSuccess) err = launch_scan_simt(u, bf16, true, st);
+    t.check = 0;
+    if (err == cudaSuccess) {
+      const dim3 grid(static_cast<unsigned>(s.batch * s.heads),
+                      static_cast<unsigned>((elems / 4 + 255) / 256), static_cast<unsigned>(u.passes));
+      state_chain_kernel<<<grid, 256, 0, st>>>(s, segment, elems, chain[0], chain[1]);
+      err = cudaGetLastError();
+    }
+  }
+  // Scans of one shape share a launch.
+  for (int i = 0; i < n && err == cudaSuccess;) {
+    ScanArgs u = t;
+    const int da = passes[i].da, dc = passes[i].dc;
+    for (; i < n && passes[i].da == da && passes[i].dc == dc; ++i) u.p[u.passes++] = passes[i];
+    u.items = slots * s.heads * u.passes;
+    err = launch_scan_simt(u, bf16, false, st);
+    t.check = 0;
+  }
+  return err;
+}
+
+}  // namespace
+}  // namespace sa
+
+extern "C" {
+
+size_t sa_workspace_bytes_linear_attention(int heads, int d_k, int d_v, int64_t batch,
+                                           int64_t total_rows, int64_t max_rows) {
+  if (heads < 1 || batch < 0 || total_rows < 0 || max_rows < 0 || !sa::width_ok(d_k) ||
+      !sa::width_ok(d_v))
+    return 0;
+  const int sms = sa::device_sms(), elems = d_k * d_v;
+  if (sms == 0) return 0;
+  size_t most = 0;
+  for (int scans = 1; scans <= 3; scans += 2) {
+    const int64_t seg =
+        sa::split_rows(sa::kSplitSimt, batch, total_rows, max_rows, heads, scans, sms);
+    const size_t n = seg == 0 ? 0
+                     : scans == 1 ? 2 * sa::bound_bytes(total_rows, seg, heads, elems) +
+                                        sa::state_bytes(batch, heads, elems)
+                                  : 2 * sa::bound_bytes(total_rows, seg, heads, elems);
+    if (n > most) most = n;
+  }
+  return sa::kWsHeaderBytes + most;
+}
+
+sa_status sa_linear_attention_forward(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                                      int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                                      int64_t v_head, const float* log_decay,
+                                      const int64_t* offsets, int64_t batch, int64_t total_rows,
+                                      int64_t max_rows, int heads, int d_k, int d_v,
+                                      sa_dtype dtype, float scale, const float* initial_state,
+                                      void* out, float* final_state, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  const sa::ScanInput iq = {q, q_row, q_head}, ik = {k, k_row, k_head}, iv = {v, v_row, v_head};
+  const sa::ScanCommon s = {log_decay, offsets, batch, total_rows, heads,
+                            static_cast<sa::WsHeader*>(workspace)};
+  if (!sa::common_ok(s, d_k, d_v, dtype, scale) || max_rows < 0) return SA_ERR_INVALID_ARG;
+  const size_t e = dtype == SA_BF16 ? 2 : 4;
+  if (!sa::input_ok(iq, heads, d_k, e) || !sa::input_ok(ik, heads, d_k, e) ||
+      !sa::input_ok(iv, heads, d_v, e) || !sa::al(out, 16) || !sa::al(initial_state, 16) ||
+      !sa::al(final_state, 16) || workspace == nullptr || !sa::al(workspace, 256))
+    return SA_ERR_INVALID_ARG;
+  if (total_rows > 0 && (q == nullptr || k == nullptr || v == nullptr || out == nullptr))
+    return SA_ERR_INVALID_ARG;
+  if (batch == 0) return total_rows == 0 ? SA_OK : SA_ERR_INVALID_ARG;
+  const sa_status dev = sa::on_sm100();
+  if (dev != SA_OK) return dev;
+  if (workspace_bytes <
+      sa_workspace_bytes_linear_attention(heads, d_k, d_v, batch, total_rows, max_rows))
+    return SA_ERR_WORKSPACE;
+  sa::ScanPass p = {};
+  p.a = iq, p.b = ik, p.c = iv, p.da = d_k, p.dc = d_v;
+  p.ends = initial_state, p.ends_mul = 1.f;
+  p.out = out, p.out_mul = scale;
+  p.fin = final_state, p.fin_mul = 1.f;
+  return sa::run_scans(&p, 1, s, max_rows, d_k, d_v, dtype == SA_BF16, sa::device_sms(),
+                       static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SA_OK
+             : SA_ERR_CUDA;
+}
+
+sa_status sa_linear_attention_backward(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                                       int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                                       int64_t v_head, const float* log_decay,
+                                       const int64_t* offsets, int64_t batch, int64_t total_rows,
+                                       int64_t max_rows, int heads, int d_k, int d_v,
+                                       sa_dtype dtype, float scale, const float* initial_state,
+                                       const void* d_out, int64_t d_out_row, int64_t d_out_head,
+                                       const float* d_final_state, void* dq, void* dk, void* dv,
+                                       float* d_initial_state, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  const sa::ScanInput iq = {q, q_row, q_head}, ik = {k, k_row, k_head}, iv = {v, v_row, v_head};
+  const sa::ScanInput ig = {d_out, d_out_row, d_out_head};
+  const sa::ScanCommon s = {log_decay, offsets, batch, total_rows, heads,
+                            static_cast<sa::WsHeader*>(workspace)};
+  if (!sa::common_ok(s, d_k, d_v, dtype, scale) || max_rows < 0) return SA_ERR_INVALID_ARG;
+  const size_t e = dtype == SA_BF16 ? 2 : 4;
+  if (!sa::input_ok(iq, heads, d_k, e) || !sa::input_ok(ik, heads, d_k, e) ||
+      !sa::input_ok(iv, heads, d_v, e) || !sa::input_ok(ig, heads, d_v, e) || !sa::al(dq, 16) ||
+      !sa::al(dk, 16) || !sa::al(dv, 16) || !sa::al(initial_state, 16) ||
+      !sa::al(d_final_state, 16) || !sa::al(d_initial_state, 16) || workspace == nullptr ||
+      !sa::al(workspace, 256))
+    return SA_ERR_INVALID_ARG;
+  if (total_rows > 0 && (q == nullptr || k == nullptr || v == nullptr || d_out == nullptr ||
+                         dq == nullptr || dk == nullptr || dv == nullptr))
+    return SA_ERR_INVALID_ARG;
+  if (batch == 0) return total_rows == 0 ? SA_OK : SA_ERR_INVALID_ARG;
+  const sa_status dev = sa::on_sm100();
+  if (dev != SA_OK) return dev;
+  if (workspace_bytes <
+      sa_workspace_bytes_linear_attention(heads, d_k, d_v, batch, total_rows, max_rows))
+    return SA_ERR_WORKSPACE;
+  const float inv = 1.f / scale;
+  sa::ScanPass p[3] = {};
+  p[0].a = ig, p[0].b = iv, p[0].c = ik, p[0].out = dq;
+  p[0].ends = initial_state, p[0].ends_mul = 1.f;
+  p[1].a = iv, p[1].b = ig, p[1].c = iq, p[1].out = dk;
+  p[2].a = ik, p[2].b = iq, p[2].c = ig, p[2].out = dv;
+  p[2].fin = d_initial_state, p[2].fin_mul = scale;
+  for (int i = 0; i < 3; ++i) {
+    p[i].transposed = i < 2;
+    p[i].da = i < 2 ? d_v : d_k, p[i].dc = i < 2 ? d_k : d_v;
+    p[i].out_mul = scale;
+    if (i > 0) p[i].reverse = 1, p[i].ends = d_final_state, p[i].ends_mul = inv;
+  }
+  return sa::run_scans(p, 3, s, max_rows, d_k, d_v, dtype == SA_BF16, sa::device_sms(),
+                       static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SA_OK
+             : SA_ERR_CUDA;
+}
+
+sa_status sa_linear_attention_step(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                                   int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                                   int64_t v_head, const float* log_decay, const int64_t* slots,
+                                   int64_t batch, int64_t states, int heads, int d_k, int d_v,
+                                   sa_dtype dtype, float scale, float* state, void* out,
+                                   uint32_t* device_flags, void* stream) {
+  const sa::ScanInput iq = {q, q_row, q_head}, ik = {k, k_row, k_head}, iv = {v, v_row, v_head};
+  if (batch < 0 || batch >= (int64_t{1} << 31) / 1024 || states < 0 || heads < 1 || heads > 1024 ||
+      d_k < 1 || d_k > sa::kStepMaxWidth || d_v < 4 || d_v > sa::kStepMaxWidth || d_v % 4 != 0 ||
+      (dtype != SA_BF16 && dtype != SA_FP32) || !isfinite(scale) ||
+      (slots == nullptr && states < batch))
+    return SA_ERR_INVALID_ARG;
+  const size_t e = dtype == SA_BF16 ? 2 : 4;
+  if (!sa::input_ok(iq, heads, d_k, e) || !sa::input_ok(ik, heads, d_k, e) ||
+      !sa::input_ok(iv, heads, d_v, e) || !sa::al(slots, 8) || !sa::al(log_decay, 4) ||
+      !sa::al(state, 16) || !sa::al(out, e) || !sa::al(device_flags, 4))
+    return SA_ERR_INVALID_ARG;
+  if (batch == 0) return SA_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || log_decay == nullptr || out == nullptr ||
+      (states > 0 && state == nullptr))
+    return SA_ERR_INVALID_ARG;
+  const sa_status dev = sa::on_sm100();
+  if (dev != SA_OK) return dev;
+  sa::StepArgs a = {iq, ik, iv, log_decay, slots, batch, states, state, out, heads, d_k, d_v, 0,
+                    scale, device_flags};
+  // Whole state rows per block when there are blocks for every SM; else 32
+  // columns per block, which gives up to eight times as many.
+  const int all4 = d_v / 4;
+  a.cols4 = batch * heads >= 296 ? all4 : all4 < 8 ? all4 : 8;
+  const dim3 grid(static_cast<unsigned>(batch * heads), static_cast<unsigned>((all4 + a.cols4 - 1) / a.cols4));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == SA_BF16) sa::step_kernel<uint16_t><<<grid, sa::kStepThreads, 0, st>>>(a);
+  else sa::step_kernel<float><<<grid, sa::kStepThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // extern "C"
