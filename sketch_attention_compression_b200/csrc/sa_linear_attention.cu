@@ -200,6 +200,13 @@ bool input_ok(const ScanInput& in, int heads, int d, size_t elem) {
          (heads == 1 || in.head >= d);
 }
 
+// A stride that no element needs (one head, one row) as a dense tensor has it.
+ScanInput dense_where_free(ScanInput in, int64_t rows, int heads, int d) {
+  if (heads == 1) in.head = d;
+  if (rows == 1) in.row = static_cast<int64_t>(heads) * d;
+  return in;
+}
+
 bool common_ok(const ScanCommon& s, int dk, int dv, sa_dtype dtype, float scale) {
   return s.batch >= 0 && s.batch < (int64_t{1} << 31) / 1024 && s.rows >= 0 &&
          s.rows < (int64_t{1} << 31) - 256 && s.heads >= 1 && s.heads <= 1024 && width_ok(dk) &&
@@ -225,7 +232,7 @@ sa_status on_sm100() {
 struct SplitRule {
   int64_t tile, least, launches;  // rows: chunk, shortest segment, the extra launches' worth
 };
-constexpr SplitRule kSplitSimt = {64, 64, 32};
+constexpr SplitRule kSplitSimt = {64, 64, 32}, kSplitTc = {128, 512, 1024};
 
 int64_t split_rows(const SplitRule& rule, int64_t batch, int64_t rows, int64_t max_rows, int heads,
                    int scans, int sms) {
@@ -262,10 +269,18 @@ int device_sms() {
 // Runs n scans (n = 1: the forward; n = 3: dq, dk, dv) of one batch.  The
 // workspace: header | states between segments, forward, reverse | a copy of
 // the initial states (forward scans whose final states replace them).
-cudaError_t run_scans(ScanPass* passes, int n, const ScanCommon& s, int64_t max_rows, int d_k,
-                      int d_v, bool bf16, int sms, cudaStream_t st) {
-  const int elems = d_k * d_v;
-  const int64_t segment = split_rows(kSplitSimt, s.batch, s.rows, max_rows, s.heads, n, sms);
+// `inputs` are q, k, v and, for the gradients, d_out.
+cudaError_t run_scans(ScanPass* passes, int n, const ScanInput* inputs, const ScanCommon& s,
+                      int64_t max_rows, int d_k, int d_v, bool bf16, int sms, cudaStream_t st) {
+  const int elems = d_k * d_v, operands = n == 3 ? 4 : 3;
+  bool tc = bf16 && s.rows > 0;
+  ScanMaps maps = {};
+  for (int i = 0; i < operands; ++i) tc = tc && scan_tc_usable(inputs[i]);
+  for (int i = 0; tc && i < operands; ++i)
+    tc = make_tmap_bf16_heads(&maps.m[i], inputs[i].p, s.rows, s.heads, i < 2 ? d_k : d_v,
+                              inputs[i].row, inputs[i].head, 128);
+  const int64_t segment = split_rows(tc ? kSplitTc : kSplitSimt, s.batch, s.rows, max_rows, s.heads,
+                                     n, sms);
   uint8_t* ws = reinterpret_cast<uint8_t*>(s.header) + kWsHeaderBytes;
   const size_t half = bound_bytes(s.rows, segment, s.heads, elems);
   for (int i = 0; i < n; ++i) passes[i].bound = reinterpret_cast<float*>(ws + passes[i].reverse * half);
@@ -274,13 +289,27 @@ cudaError_t run_scans(ScanPass* passes, int n, const ScanCommon& s, int64_t max_
   t.check = 1;
   t.segment = segment == 0 ? s.rows + 1 : segment;
   const int64_t slots = s.batch + (segment == 0 ? 0 : s.rows / segment);
+  // The tensor-core scan's item counters live in the header, behind its flag
+  // words; they are needed where an SM takes more than one item.
+  unsigned long long* counter = nullptr;
   cudaError_t err = cudaSuccess;
+  if (tc && slots * s.heads * n > sms) {
+    counter = reinterpret_cast<unsigned long long*>(s.header) + 8;
+    err = cudaMemsetAsync(s.header, 0, kWsHeaderBytes, st);
+  }
+  auto launch = [&](ScanArgs& u, bool states_only) {
+    u.items = slots * s.heads * u.passes;
+    if (!tc) return launch_scan_simt(u, bf16, states_only, st);
+    if (counter != nullptr) u.counter = counter++;
+    return launch_scan_tc(u, maps, states_only, sms, st);
+  };
   if (segment != 0) {
     if (n == 1 && passes[0].ends != nullptr && passes[0].ends == passes[0].fin) {
       // The last segment's final state must not meet the first one's start.
       void* copy = ws + 2 * half;
-      err = cudaMemcpyAsync(copy, passes[0].ends, static_cast<size_t>(s.batch) * s.heads * elems * 4,
-                            cudaMemcpyDeviceToDevice, st);
+      if (err == cudaSuccess)
+        err = cudaMemcpyAsync(copy, passes[0].ends, static_cast<size_t>(s.batch) * s.heads * elems * 4,
+                              cudaMemcpyDeviceToDevice, st);
       passes[0].ends = static_cast<const float*>(copy);
     }
     // The states of the forward direction are sums over k and v, those of
@@ -298,8 +327,7 @@ cudaError_t run_scans(ScanPass* passes, int n, const ScanCommon& s, int64_t max_
       o.da = d_k, o.dc = d_v;
       chain[p.reverse] = {p.reverse, p.ends, p.ends_mul, p.bound};
     }
-    u.items = slots * s.heads * u.passes;
-    if (err == cudaSuccess) err = launch_scan_simt(u, bf16, true, st);
+    if (err == cudaSuccess) err = launch(u, true);
     t.check = 0;
     if (err == cudaSuccess) {
       const dim3 grid(static_cast<unsigned>(s.batch * s.heads),
@@ -313,8 +341,7 @@ cudaError_t run_scans(ScanPass* passes, int n, const ScanCommon& s, int64_t max_
     ScanArgs u = t;
     const int da = passes[i].da, dc = passes[i].dc;
     for (; i < n && passes[i].da == da && passes[i].dc == dc; ++i) u.p[u.passes++] = passes[i];
-    u.items = slots * s.heads * u.passes;
-    err = launch_scan_simt(u, bf16, false, st);
+    err = launch(u, false);
     t.check = 0;
   }
   return err;
@@ -333,9 +360,10 @@ size_t sa_workspace_bytes_linear_attention(int heads, int d_k, int d_v, int64_t 
   const int sms = sa::device_sms(), elems = d_k * d_v;
   if (sms == 0) return 0;
   size_t most = 0;
-  for (int scans = 1; scans <= 3; scans += 2) {
-    const int64_t seg =
-        sa::split_rows(sa::kSplitSimt, batch, total_rows, max_rows, heads, scans, sms);
+  for (int i = 0; i < 4; ++i) {  // either kernel, either direction
+    const int scans = i < 2 ? 1 : 3;
+    const int64_t seg = sa::split_rows(i % 2 == 0 ? sa::kSplitSimt : sa::kSplitTc, batch, total_rows,
+                                       max_rows, heads, scans, sms);
     const size_t n = seg == 0 ? 0
                      : scans == 1 ? 2 * sa::bound_bytes(total_rows, seg, heads, elems) +
                                         sa::state_bytes(batch, heads, elems)
@@ -371,11 +399,17 @@ sa_status sa_linear_attention_forward(const void* q, int64_t q_row, int64_t q_he
       sa_workspace_bytes_linear_attention(heads, d_k, d_v, batch, total_rows, max_rows))
     return SA_ERR_WORKSPACE;
   sa::ScanPass p = {};
-  p.a = iq, p.b = ik, p.c = iv, p.da = d_k, p.dc = d_v;
+  p.da = d_k, p.dc = d_v;
   p.ends = initial_state, p.ends_mul = 1.f;
   p.out = out, p.out_mul = scale;
   p.fin = final_state, p.fin_mul = 1.f;
-  return sa::run_scans(&p, 1, s, max_rows, d_k, d_v, dtype == SA_BF16, sa::device_sms(),
+  p.map_a = 0, p.map_b = 1, p.map_c = 2;
+  p.parts = final_state != nullptr ? 3 : 2;
+  const sa::ScanInput inputs[3] = {sa::dense_where_free(iq, total_rows, heads, d_k),
+                                   sa::dense_where_free(ik, total_rows, heads, d_k),
+                                   sa::dense_where_free(iv, total_rows, heads, d_v)};
+  p.a = inputs[0], p.b = inputs[1], p.c = inputs[2];
+  return sa::run_scans(&p, 1, inputs, s, max_rows, d_k, d_v, dtype == SA_BF16, sa::device_sms(),
                        static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SA_OK
              : SA_ERR_CUDA;
@@ -414,18 +448,25 @@ sa_status sa_linear_attention_backward(const void* q, int64_t q_row, int64_t q_h
     return SA_ERR_WORKSPACE;
   const float inv = 1.f / scale;
   sa::ScanPass p[3] = {};
-  p[0].a = ig, p[0].b = iv, p[0].c = ik, p[0].out = dq;
+  const sa::ScanInput inputs[4] = {sa::dense_where_free(iq, total_rows, heads, d_k),
+                                   sa::dense_where_free(ik, total_rows, heads, d_k),
+                                   sa::dense_where_free(iv, total_rows, heads, d_v),
+                                   sa::dense_where_free(ig, total_rows, heads, d_v)};
+  const int which[3][3] = {{3, 2, 1}, {2, 3, 0}, {1, 0, 3}};  // dq, dk, dv
+  void* const out[3] = {dq, dk, dv};
   p[0].ends = initial_state, p[0].ends_mul = 1.f;
-  p[1].a = iv, p[1].b = ig, p[1].c = iq, p[1].out = dk;
-  p[2].a = ik, p[2].b = iq, p[2].c = ig, p[2].out = dv;
   p[2].fin = d_initial_state, p[2].fin_mul = scale;
   for (int i = 0; i < 3; ++i) {
+    p[i].map_a = which[i][0], p[i].map_b = which[i][1], p[i].map_c = which[i][2];
+    p[i].a = inputs[p[i].map_a], p[i].b = inputs[p[i].map_b], p[i].c = inputs[p[i].map_c];
+    p[i].out = out[i];
+    p[i].parts = p[i].fin != nullptr ? 3 : 2;
     p[i].transposed = i < 2;
     p[i].da = i < 2 ? d_v : d_k, p[i].dc = i < 2 ? d_k : d_v;
     p[i].out_mul = scale;
     if (i > 0) p[i].reverse = 1, p[i].ends = d_final_state, p[i].ends_mul = inv;
   }
-  return sa::run_scans(p, 3, s, max_rows, d_k, d_v, dtype == SA_BF16, sa::device_sms(),
+  return sa::run_scans(p, 3, inputs, s, max_rows, d_k, d_v, dtype == SA_BF16, sa::device_sms(),
                        static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SA_OK
              : SA_ERR_CUDA;

@@ -184,4 +184,13 @@ __device__ __forceinline__ void check_inputs(const ScanCommon& s, uint32_t* shar
 // written to p[].bound) on the CUDA cores (sa_linear_attention_simt.cu).
 cudaError_t launch_scan_simt(const ScanArgs& t, bool bf16, bool states_only, cudaStream_t st);
 
+// The same on the tensor cores (sa_linear_attention_tc.cu), bf16 inputs whose
+// tensor maps the passes name.
+struct ScanMaps {
+  CUtensorMap m[4];
+};
+cudaError_t launch_scan_tc(const ScanArgs& t, const ScanMaps& maps, bool states_only, int sms,
+                           cudaStream_t st);
+bool scan_tc_usable(const ScanInput& in);  // addresses and strides that TMA takes
+
 }  // namespace sa

@@ -1,0 +1,612 @@
+// Linear attention with a decay per head on the tensor cores (bf16 inputs).
+// The scans and their formulas are in sa_linear_attention.h.  Chunks have 128
+// rows; per chunk, with all operands in shared memory:
+//
+//   M1  P  = a b^T                    M 128, N 128, K da
+//       P~ = P weighted and masked    (bf16, TMEM)
+//   M2  O2 = a S~                     M 128, N dc,  K da   (S~: S in bf16)
+//   M3  O1 = P~ c                     M 128, N dc,  K 128  (A from TMEM)
+//   M4  D  = (w b)^T c                M da,  N dc,  K 128, w_j = l^(L-1-r_j)
+//       out = mul (O1 + l^(r+1) O2);  S <- l^L S + D
+//
+// Roundings to bf16: P~ and S~, the operands of an output that is bf16
+// itself.  S is kept in fp32 registers: w b is split into bf16 parts whose
+// products are all accumulated, three parts (24 significant bits) where the
+// state itself is an answer, two (16 bits) where only S~ is taken from it;
+// each chunk's D starts from zero and is added to S in registers, so that
+// long sums are not left to the accumulator's rounding.
+//
+// One persistent CTA per SM: warp 0 fetches work items and loads tiles (TMA,
+// two stages), warp 1 issues the MMAs, warps 4-11 do the rest, two warps per
+// TMEM lane quarter, each with half of the columns.  Per chunk they
+//   s1  add D of the chunk before to S and store S~
+//   s2  turn P into P~ (TMEM to TMEM), while M2 runs
+//   s3  split w b into the stage's own b and a tiles (M1 and M2 have read
+//       them) and S~'s place, while M3 runs
+//   s4  store out, while M4 and the next chunk's M1 run.
+// TMEM: P and P~ at 0, O1 at 128, O2 at 256, D at 384.  Shared memory at
+// da = dc = 128: two stages of three 32 KB tiles and 32 KB for S~: 224 KB.
+//
+// A product of P~ = 0 with a c that is not finite is NaN, so a row could see
+// such a value in its future.  An output whose O1 is not finite although
+// the state's share is, is summed again over the rows that it may see.
+#include <cuda_bf16.h>
+
+#include "sa.h"
+#include "sa_internal.h"
+#include "sa_linear_attention.h"
+#include "sa_ptx.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kCompute = 256;  // threads of warps 4-11
+constexpr int kStages = 2, kRing = 4;
+constexpr int kBox = 128 * 128;  // 128 rows x 64 bf16
+constexpr int kTable = 132;      // l^0 .. l^128, then l^128's rounding error
+
+template <int DA, int DC>
+struct TcPlan {
+  static constexpr int kA = 0;                          // within a stage
+  static constexpr int kB = kA + (DA / 64) * kBox;
+  static constexpr int kC = kB + (DA / 64) * kBox;
+  static constexpr int kStage = kC + (DC / 64) * kBox;
+  static constexpr int kS = kStages * kStage;           // S~: dc / 64 boxes of da rows
+  static constexpr int kSBox = DA * 128;
+  static constexpr int kTab = kS + 2 * kBox;            // two tables of the decay's powers
+  static constexpr int kItems = kTab + 2 * kTable * 4;
+  static constexpr int kBars = kItems + kRing * 64;
+  // M4 with da = 64 reads a second box behind each part that is not the
+  // part's: those rows of D are never used, and the reads stay inside the
+  // stages and S~'s two boxes.
+  static constexpr int kUsed = kBars + 256;
+  // At least 116 KB, so that one CTA holds an SM (it allocates all of TMEM).
+  static constexpr int kSmem = kUsed > 118784 ? kUsed : 118784;
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kItems % 16 == 0 && kBars % 8 == 0, "alignment");
+  static_assert(kB + 2 * kBox <= kStage, "second box of b inside its stage");
+  static_assert((DC / 64) * kSBox <= 2 * kBox, "S~ in its place");
+};
+
+static_assert(sizeof(ScanItem) <= 64, "ring entry");
+
+constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256, kColD = 384;
+
+__device__ __forceinline__ uint32_t swz(int r, int u) {
+  return (r >> 3) * 1024 + (r & 7) * 128 + ((u ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// O1 of one output, over the rows that the scan has reached: for outputs that
+// values behind the mask have spoiled.
+__device__ __noinline__ float masked_sum(const ScanPass& p, int head, int64_t r0, int L, int i,
+                                         int col, const float* power) {
+  auto at = [&](const ScanInput& in, int r, int c) {
+    return bf_lo(static_cast<const uint16_t*>(
+        in.p)[(r0 + r) * in.row + static_cast<int64_t>(head) * in.head + c]);
+  };
+  float sum = 0.f;
+  for (int j = p.reverse ? i : 0; j < (p.reverse ? L : i + 1); ++j) {
+    float x = 0.f;
+    for (int d = 0; d < p.da; ++d) x = fmaf(at(p.a, i, d), at(p.b, j, d), x);
+    sum = fmaf(x * power[p.reverse ? j - i : i - j], at(p.c, j, col), sum);
+  }
+  return sum;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
+                                          volatile uint32_t* abort_flag, uint32_t* sticky) {
+  const bool ok = mbar_wait(bar, parity, abort_flag, sticky);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+template <int DA, int DC, bool STATE>
+__global__ void __launch_bounds__(kThreads, 1)
+    scan_tc_kernel(const __grid_constant__ ScanMaps maps, const __grid_constant__ ScanArgs t) {
+  using Pl = TcPlan<DA, DC>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint32_t check_flags;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (blockIdx.x == 0 && tid == 0) {
+      t.s.header->flags = 0u;
+      t.s.header->timeout_flags = DEVFLAG_SMEM_ALIGN;
+    }
+    return;
+  }
+  if (t.check && blockIdx.x == 0) check_inputs(t.s, &check_flags);
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Pl::kBars);
+  uint64_t* full = bars;                   // [2] a stage's tiles have landed
+  uint64_t* empty = bars + 2;              // [2] a stage's products are done
+  uint64_t* item_full = bars + 4;          // [4]
+  uint64_t* item_empty = bars + 8;         // [4]
+  uint64_t* p_full = bars + 12;            // M1 done
+  uint64_t* s_ready = bars + 13;           // S~ stored, D read
+  uint64_t* a_free = bars + 14;            // M2 done (and M1)
+  uint64_t* p_ready = bars + 15;           // P~ stored
+  uint64_t* b_ready = bars + 16;           // w b stored
+  uint64_t* o_full = bars + 17;            // M3 done (and M2)
+  uint64_t* d_full = bars + 18;            // M4 done
+  uint64_t* tab_ready = bars + 19;         // a table of powers stored
+  uint64_t* drain = bars + 20;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(item_full + i, 1);
+      mbar_init(item_empty + i, 9);
+    }
+    mbar_init(p_full, 1);
+    mbar_init(s_ready, 8);
+    mbar_init(a_free, 1);
+    mbar_init(p_ready, 8);
+    mbar_init(b_ready, 8);
+    mbar_init(o_full, 1);
+    mbar_init(d_full, 1);
+    mbar_init(tab_ready, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  uint32_t* sticky = &t.s.header->timeout_flags;
+  const uint32_t tmem = *tmem_slot;
+
+  // The next item from the ring; false at the end (hi < lo) or on abort.
+  uint32_t ri = 0;  // ring entries taken
+  auto take = [&](ScanItem& it, bool& ok) -> bool {
+    ok = ok && warp_wait(item_full + ri % kRing, (ri / kRing) & 1u, abort_flag, sticky);
+    if (!ok) return false;
+    const volatile ScanItem* e = reinterpret_cast<const volatile ScanItem*>(smem + Pl::kItems + (ri % kRing) * 64);
+    it.lo = e->lo, it.hi = e->hi, it.state = e->state, it.from = e->from, it.to = e->to;
+    it.head = e->head, it.pass = e->pass, it.first = e->first, it.last = e->last;
+    warp_arrive(item_empty + ri % kRing, lane);
+    ++ri;
+    return it.hi >= it.lo;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ items and TMA loads
+    bool ok = true;
+    uint32_t n = 0;  // chunks loaded
+    int64_t next = blockIdx.x;
+    while (ok) {
+      if (t.counter != nullptr) {
+        unsigned long long x = 0;
+        if (lane == 0) x = atomicAdd(t.counter, 1ull);
+        next = static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, x, 0));
+      }
+      ScanItem it;
+      const bool end = next >= t.items;
+      const bool some = !end && item_of(t, next, lane, STATE, it);
+      next += gridDim.x;
+      if (!end && !some) continue;
+      if (end) it.lo = 0, it.hi = -1;
+      if (ri >= kRing) ok = warp_wait(item_empty + ri % kRing, (ri / kRing + 1) & 1u, abort_flag, sticky);
+      if (!ok) break;
+      if (lane == 0) {
+        volatile ScanItem* e = reinterpret_cast<volatile ScanItem*>(smem + Pl::kItems + (ri % kRing) * 64);
+        e->lo = it.lo, e->hi = it.hi;
+        if (!end) {
+          e->state = it.state, e->from = it.from, e->to = it.to;
+          e->head = it.head, e->pass = it.pass, e->first = it.first, e->last = it.last;
+        }
+        mbar_arrive(item_full + ri % kRing);
+      }
+      ++ri;
+      if (end) break;
+      const ScanPass& p = t.p[it.pass];
+      const int64_t chunks = (it.hi - it.lo + 127) / 128;
+      for (int64_t c = 0; c < chunks && ok; ++c, ++n) {
+        const uint32_t st = n % kStages;
+        if (n >= kStages) ok = warp_wait(empty + st, (n / kStages + 1) & 1u, abort_flag, sticky);
+        if (!ok) break;
+        if (lane == 0) {
+          const int32_t y = it.head;
+          const int32_t z = static_cast<int32_t>(it.lo + 128 * (p.reverse ? chunks - 1 - c : c));
+          uint8_t* d = smem + st * Pl::kStage;
+          mbar_arrive_expect_tx(full + st, ((STATE ? 1 : 2) * (DA / 64) + DC / 64) * kBox);
+#pragma unroll
+          for (int b = 0; b < DA / 64; ++b) {
+            if (!STATE) tma_load_3d(d + Pl::kA + b * kBox, &maps.m[p.map_a], full + st, b * 64, y, z);
+            tma_load_3d(d + Pl::kB + b * kBox, &maps.m[p.map_b], full + st, b * 64, y, z);
+          }
+#pragma unroll
+          for (int b = 0; b < DC / 64; ++b)
+            tma_load_3d(d + Pl::kC + b * kBox, &maps.m[p.map_c], full + st, b * 64, y, z);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) {
+      // Let the copies in flight land before the CTA releases its memory.
+      for (uint32_t k = (n >= kStages ? n - kStages : 0); k < n; ++k)
+        mbar_wait_bounded(full + k % kStages, (k / kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    bool ok = true;
+    constexpr uint32_t id_p = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t id_o = idesc_bf16_f32(128, DC, 0, 1);
+    constexpr uint32_t id_d = idesc_bf16_f32(128, DC, 1, 1);
+    uint32_t n = 0;
+    auto m1 = [&](uint32_t c) {
+      const uint32_t d = sbase + (c % kStages) * Pl::kStage;
+      const uint64_t da = smem_desc(d + Pl::kA, 16, 1024, 2), db = smem_desc(d + Pl::kB, 16, 1024, 2);
+#pragma unroll
+      for (int ks = 0; ks < DA / 16; ++ks) {
+        const uint64_t o = ((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
+        mma_bf16_ss(tmem + kColP, da + o, db + o, id_p, ks > 0 ? 1u : 0u);
+      }
+      mma_commit(p_full);
+    };
+    ScanItem it;
+    while (take(it, ok)) {
+      const int64_t chunks = (it.hi - it.lo + 127) / 128;
+      bool ahead = false;  // M1 of this chunk already issued
+      for (int64_t c = 0; c < chunks && ok; ++c, ++n) {
+        const uint32_t st = n % kStages, ph = n & 1u;
+        const uint32_t d = sbase + st * Pl::kStage;
+        const uint64_t cm = smem_desc(d + Pl::kC, kBox, 1024, 2);  // c, MN-major B
+        bool next = false;
+        if (!STATE) {
+          if (!ahead) {
+            if (!warp_wait(full + st, (n / kStages) & 1u, abort_flag, sticky)) { ok = false; break; }
+            tc_fence_after();
+            if (lane == 0) m1(n);
+          }
+          if (!warp_wait(s_ready, ph, abort_flag, sticky)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t da = smem_desc(d + Pl::kA, 16, 1024, 2);
+            const uint64_t sm = smem_desc(sbase + Pl::kS, Pl::kSBox, 1024, 2);
+#pragma unroll
+            for (int ks = 0; ks < DA / 16; ++ks)
+              mma_bf16_ss(tmem + kColO2, da + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4),
+                          sm + ((ks * 2048) >> 4), id_o, ks > 0 ? 1u : 0u);
+            mma_commit(a_free);
+          }
+          if (!warp_wait(p_ready, ph, abort_flag, sticky)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ts(tmem + kColO1, tmem + kColP + (ks >> 2) * 64 + (ks & 3) * 8,
+                          cm + ((ks * 2048) >> 4), id_o, ks > 0 ? 1u : 0u);
+            mma_commit(o_full);
+          }
+          // The next chunk's M1 goes before this chunk's M4 if its tiles are there.
+          if (c + 1 < chunks) {
+            next = __all_sync(0xFFFFFFFFu,
+                              mbar_test_wait(full + (n + 1) % kStages, ((n + 1) / kStages) & 1u));
+            if (next) {
+              tc_fence_after();
+              if (lane == 0) m1(n + 1);
+            }
+          }
+        }
+        if (!warp_wait(b_ready, ph, abort_flag, sticky)) { ok = false; break; }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t hi = smem_desc(d + Pl::kB, kBox, 1024, 2);  // w b, MN-major A
+          const uint64_t lo = smem_desc(d + Pl::kA, kBox, 1024, 2);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_ss(tmem + kColD, hi + ((ks * 2048) >> 4), cm + ((ks * 2048) >> 4), id_d,
+                        ks > 0 ? 1u : 0u);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_ss(tmem + kColD, lo + ((ks * 2048) >> 4), cm + ((ks * 2048) >> 4), id_d, 1u);
+          if (t.p[it.pass].parts == 3) {
+            const uint64_t low = smem_desc(sbase + Pl::kS, kBox, 1024, 2);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ss(tmem + kColD, low + ((ks * 2048) >> 4), cm + ((ks * 2048) >> 4), id_d, 1u);
+          }
+          mma_commit(empty + st);
+          mma_commit(d_full);
+        }
+        __syncwarp();
+        ahead = next;
+      }
+    }
+    if (!ok && lane == 0) {
+      mma_commit(drain);
+      mbar_wait_bounded(drain, 0);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ decay, state, output
+    bool ok = true;
+    const int q = warp & 3, hf = (warp - 4) >> 2, ctid = tid - 128;
+    const int row = q * 32 + lane;  // TMEM lane: row of the chunk, row of the state
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t tab = sbase + Pl::kTab, items = 0;
+    constexpr int HC = DC / 2;
+    const bool state_row = DA == 128 || q < 2;
+    float S[HC];
+    uint32_t n = 0;
+    ScanItem it;
+    auto power = [&](int e) { return ld_shared_f32(tab + e * 4); };
+    // S <- (f + fl) S + D, once M4 of the chunk before is done.
+    auto add_d = [&](float f, float fl) {
+      if (!ok || !warp_wait(d_full, (n - 1) & 1u, abort_flag, sticky)) {
+        ok = false;
+        return;
+      }
+      tc_fence_after();
+      if (state_row) {
+#pragma unroll
+        for (int j = 0; j < HC / 32; ++j) {
+          uint32_t v[32];
+          tmem_ld32(lane_base + kColD + hf * HC + j * 32, v);
+          tmem_wait_ld();
+          tmem_pin32(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            S[j * 32 + e] = fmaf(f, S[j * 32 + e], fmaf(fl, S[j * 32 + e], __uint_as_float(v[e])));
+        }
+      }
+      tc_fence_before();
+    };
+    while (take(it, ok)) {
+      const ScanPass& p = t.p[it.pass];
+      const bool rev = p.reverse != 0;
+      // The decay's powers, in one of two tables: a warp that writes a table
+      // has seen tab_ready of the item before, so every warp has left the
+      // item before that one, which used the same table.
+      const double g = static_cast<double>(usable_decay(__ldg(t.s.log_decay + it.head)));
+      tab = sbase + Pl::kTab + (items & 1u) * (kTable * 4);
+      float* table = reinterpret_cast<float*>(smem + Pl::kTab) + (items & 1u) * kTable;
+      if (ctid <= 128) {
+        const double w = exp(g * ctid);
+        table[ctid] = static_cast<float>(w);
+        if (ctid == 128) table[129] = static_cast<float>(w - static_cast<float>(w));
+      }
+      warp_arrive(tab_ready, lane);
+      // The state to start from.
+      if (state_row) {
+        const bool seg = !STATE && it.from >= 0;
+        const float* src = STATE ? nullptr : seg ? p.bound : p.ends;
+        const float m = seg ? 1.f : p.ends_mul;
+        const bool tr = p.transposed != 0;
+        const int64_t o = (seg ? it.from : it.state) * (DA * DC);
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+          const int col = hf * HC + j;
+          S[j] = src == nullptr ? 0.f : m * src[o + (tr ? col * DA + row : row * DC + col)];
+        }
+      }
+      if (!warp_wait(tab_ready, items & 1u, abort_flag, sticky)) break;
+      ++items;
+      const int64_t chunks = (it.hi - it.lo + 127) / 128;
+      float f = 0.f, fl = 0.f;  // decay of S over the chunk before
+      for (int64_t c = 0; c < chunks && ok; ++c, ++n) {
+        const uint32_t st = n % kStages, ph = n & 1u;
+        uint8_t* d = smem + st * Pl::kStage;
+        const int64_t r0 = it.lo + 128 * (rev ? chunks - 1 - c : c);
+        const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
+        // A reverse scan's first chunk of a user takes the start state undecayed.
+        const int skip = rev && it.first && c == 0 ? 1 : 0;
+        // s1
+        if (c > 0) add_d(f, fl);
+        if (!ok) break;
+        f = power(L - skip);
+        fl = L - skip == 128 ? power(129) : 0.f;
+        if (!STATE && state_row) {
+#pragma unroll
+          for (int u = 0; u < HC / 8; ++u) {
+            const int col = hf * HC + u * 8;
+            st_shared_v4(sbase + Pl::kS + (col >> 6) * Pl::kSBox + swz(row, (col & 63) >> 3),
+                         pack_bf16x2(S[u * 8], S[u * 8 + 1]), pack_bf16x2(S[u * 8 + 2], S[u * 8 + 3]),
+                         pack_bf16x2(S[u * 8 + 4], S[u * 8 + 5]),
+                         pack_bf16x2(S[u * 8 + 6], S[u * 8 + 7]));
+          }
+        }
+        if (!warp_wait(full + st, (n / kStages) & 1u, abort_flag, sticky)) { ok = false; break; }
+        if (L < 128) {
+          // Rows behind the end belong to another user or to nobody: c's must
+          // not reach the sums, whatever they hold.
+          for (int e = ctid; e < (128 - L) * (DC / 8); e += kCompute) {
+            const int r = L + e / (DC / 8), u = e % (DC / 8);
+            st_shared_v4(smem_u32(d) + Pl::kC + (u >> 3) * kBox + swz(r, u & 7), 0u, 0u, 0u, 0u);
+          }
+        }
+        if (!STATE) {
+          fence_proxy_async_smem();
+          tc_fence_before();
+          warp_arrive(s_ready, lane);
+          // s2: this half's 64 columns of P, 32 at a time.  A block of 32 x
+          // 32 that the scan covers whole has the weight E F_j, both powers
+          // with exponents >= 0; the one on the diagonal is masked.
+          if (!warp_wait(p_full, ph, abort_flag, sticky)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int jb = hf * 2 + k;
+            uint32_t o[16];
+            if (rev ? jb < q : jb > q) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = 0u;
+            } else {
+              uint32_t v[32];
+              tmem_ld32(lane_base + kColP + jb * 32, v);
+              tmem_wait_ld();
+              tmem_pin32(v);
+              if (jb == q) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const int dist = rev ? e - lane : lane - e;
+                  const bool in = dist >= 0 && jb * 32 + e < L;
+                  const float w = power(in ? dist : 0);
+                  v[e] = in ? __float_as_uint(__uint_as_float(v[e]) * w) : 0u;
+                }
+              } else {
+                const float E = power(rev ? jb * 32 - row : row - jb * 32 - 31);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const float w = E * power(rev ? e : 31 - e);
+                  v[e] = jb * 32 + e < L ? __float_as_uint(__uint_as_float(v[e]) * w) : 0u;
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+            }
+            tmem_st16(lane_base + kColP + hf * 64 + k * 16, o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(p_ready, lane);
+          if (!warp_wait(a_free, ph, abort_flag, sticky)) { ok = false; break; }
+        }
+        // s3: w b in two or three bf16 parts, over b, over a and in S~'s place.
+#pragma unroll 4
+        for (int e = ctid; e < 128 * (DA / 8); e += kCompute) {
+          const int r = e / (DA / 8), u = e % (DA / 8);
+          const uint32_t o = (u >> 3) * kBox + swz(r, u & 7);
+          const uint32_t src = smem_u32(d) + Pl::kB + o, dst = smem_u32(d) + Pl::kA + o;
+          uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u}, low[4] = {0u, 0u, 0u, 0u};
+          if (r < L) {
+            const float w = power(rev ? r : L - 1 - r);
+            const uint4 x = ld_shared_v4u(src);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float y0 = w * bf_lo(xs[i]), y1 = w * bf_hi(xs[i]);
+              hi[i] = pack_bf16x2(y0, y1);
+              y0 -= bf_lo(hi[i]), y1 -= bf_hi(hi[i]);
+              lo[i] = pack_bf16x2(y0, y1);
+              low[i] = pack_bf16x2(y0 - bf_lo(lo[i]), y1 - bf_hi(lo[i]));
+            }
+          }
+          st_shared_v4(src, hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(dst, lo[0], lo[1], lo[2], lo[3]);
+          if (p.parts == 3) st_shared_v4(sbase + Pl::kS + o, low[0], low[1], low[2], low[3]);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(b_ready, lane);
+        // s4
+        if (!STATE) {
+          if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
+          tc_fence_after();
+          const float w = power(row < L ? (rev ? L - row : row + 1) - skip : 0);
+#pragma unroll
+          for (int j = 0; j < HC / 32; ++j) {
+            uint32_t x[32], y[32];
+            tmem_ld32(lane_base + kColO1 + hf * HC + j * 32, x);
+            tmem_ld32(lane_base + kColO2 + hf * HC + j * 32, y);
+            tmem_wait_ld();
+            tmem_pin32(x);
+            tmem_pin32(y);
+            if (row < L) {
+              float finite = 0.f;  // NaN if some O1 is not finite
+#pragma unroll
+              for (int e = 0; e < 32; ++e) finite = fmaf(__uint_as_float(x[e]), 0.f, finite);
+              if (finite != 0.f) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!isfinite(__uint_as_float(x[e])) && isfinite(__uint_as_float(y[e])))
+                    x[e] = __float_as_uint(masked_sum(p, it.head, r0, L, row, hf * HC + j * 32 + e, table));
+              }
+              uint4* o = reinterpret_cast<uint4*>(
+                  static_cast<uint16_t*>(p.out) + ((r0 + row) * t.s.heads + it.head) * DC + hf * HC + j * 32);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t z[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int k = e * 8 + i * 2;
+                  z[i] = pack_bf16x2(
+                      p.out_mul * fmaf(w, __uint_as_float(y[k]), __uint_as_float(x[k])),
+                      p.out_mul * fmaf(w, __uint_as_float(y[k + 1]), __uint_as_float(x[k + 1])));
+                }
+                o[e] = make_uint4(z[0], z[1], z[2], z[3]);
+              }
+            }
+          }
+          tc_fence_before();
+        }
+      }
+      if (!ok) break;
+      if (chunks > 0) add_d(f, fl);
+      if (!ok) break;
+      // The state behind the last row.
+      float* dst = nullptr;
+      float m = 1.f;
+      int64_t o = 0;
+      if (STATE) {
+        dst = p.bound;
+        o = it.to * (DA * DC);
+      } else if (it.last && p.fin != nullptr) {
+        dst = p.fin;
+        o = it.state * (DA * DC);
+        m = p.fin_mul * (rev && chunks > 0 ? power(1) : 1.f);
+      }
+      if (dst != nullptr && state_row) {
+#pragma unroll
+        for (int j = 0; j < HC; j += 4)
+          *reinterpret_cast<float4*>(dst + o + row * DC + hf * HC + j) =
+              make_float4(m * S[j], m * S[j + 1], m * S[j + 2], m * S[j + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DA, int DC, bool STATE>
+cudaError_t launch(const ScanMaps& m, const ScanArgs& t, int sms, cudaStream_t st) {
+  using Pl = TcPlan<DA, DC>;
+  cudaError_t err = cudaFuncSetAttribute(scan_tc_kernel<DA, DC, STATE>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::kSmem);
+  if (err != cudaSuccess) return err;
+  const int64_t grid = t.items < sms ? t.items : sms;
+  scan_tc_kernel<DA, DC, STATE><<<static_cast<unsigned>(grid), kThreads, Pl::kSmem, st>>>(m, t);
+  return cudaGetLastError();
+}
+
+template <bool STATE>
+cudaError_t launch_any(int da, int dc, const ScanMaps& m, const ScanArgs& t, int sms, cudaStream_t st) {
+  if (da == 64)
+    return dc == 64 ? launch<64, 64, STATE>(m, t, sms, st) : launch<64, 128, STATE>(m, t, sms, st);
+  return dc == 64 ? launch<128, 64, STATE>(m, t, sms, st) : launch<128, 128, STATE>(m, t, sms, st);
+}
+
+}  // namespace
+
+bool scan_tc_usable(const ScanInput& in) {
+  return (reinterpret_cast<uintptr_t>(in.p) & 15u) == 0 && in.row > 0 && in.row % 8 == 0 &&
+         in.head > 0 && in.head % 8 == 0;
+}
+
+cudaError_t launch_scan_tc(const ScanArgs& t, const ScanMaps& maps, bool states_only, int sms,
+                           cudaStream_t st) {
+  const int da = t.p[0].da, dc = t.p[0].dc;
+  return states_only ? launch_any<true>(da, dc, maps, t, sms, st)
+                     : launch_any<false>(da, dc, maps, t, sms, st);
+}
+
+}  // namespace sa
