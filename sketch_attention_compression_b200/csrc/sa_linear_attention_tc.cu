@@ -17,13 +17,16 @@
 // long sums are not left to the accumulator's rounding.
 //
 // One persistent CTA per SM: warp 0 fetches work items and loads tiles (TMA,
-// two stages), warp 1 issues the MMAs, warps 4-11 do the rest, two warps per
-// TMEM lane quarter, each with half of the columns.  Per chunk they
+// two stages), warp 1 issues the MMAs.  Warps 4-11 hold the state, two warps
+// per TMEM lane quarter, each with half of the columns; per chunk they
 //   s1  add D of the chunk before to S and store S~
-//   s2  turn P into P~ (TMEM to TMEM), while M2 runs
 //   s3  split w b into the stage's own b and a tiles (M1 and M2 have read
-//       them) and S~'s place, while M3 runs
+//       them) and S~'s place
+// and warps 12-15 make the output, one row of the chunk per thread:
+//   s2  turn P into P~ (TMEM to TMEM)
 //   s4  store out, while M4 and the next chunk's M1 run.
+// The chain s1, M2, s3, M4 carries the state from chunk to chunk; s2, M3 and
+// s4 run beside it.
 // TMEM: P and P~ at 0, O1 at 128, O2 at 256, D at 384.  Shared memory at
 // da = dc = 128: two stages of three 32 KB tiles and 32 KB for S~: 224 KB.
 //
@@ -40,11 +43,11 @@
 namespace sa {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kCompute = 256;  // threads of warps 4-11
+constexpr int kThreads = 512;
+constexpr int kStateThreads = 256;  // warps 4-11
 constexpr int kStages = 2, kRing = 4;
 constexpr int kBox = 128 * 128;  // 128 rows x 64 bf16
-constexpr int kTable = 132;      // l^0 .. l^128, then l^128's rounding error
+constexpr int kTable = 132;         // l^0 .. l^128, then l^128's rounding error
 
 template <int DA, int DC>
 struct TcPlan {
@@ -54,8 +57,8 @@ struct TcPlan {
   static constexpr int kStage = kC + (DC / 64) * kBox;
   static constexpr int kS = kStages * kStage;           // S~: dc / 64 boxes of da rows
   static constexpr int kSBox = DA * 128;
-  static constexpr int kTab = kS + 2 * kBox;            // two tables of the decay's powers
-  static constexpr int kItems = kTab + 2 * kTable * 4;
+  static constexpr int kTab = kS + 2 * kBox;            // four tables of the decay's powers
+  static constexpr int kItems = kTab + 4 * kTable * 4;
   static constexpr int kBars = kItems + kRing * 64;
   // M4 with da = 64 reads a second box behind each part that is not the
   // part's: those rows of D are never used, and the reads stay inside the
@@ -97,6 +100,40 @@ __device__ __noinline__ float masked_sum(const ScanPass& p, int head, int64_t r0
   return sum;
 }
 
+// Element e of packed pairs becomes x.
+__device__ __forceinline__ void put_half(uint32_t (&z)[16], int e, float x) {
+  const uint32_t w = pack_bf16x2(x, x), mask = e & 1 ? 0xFFFF0000u : 0xFFFFu;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = e / 2 == i ? (z[i] & ~mask) | (w & mask) : z[i];
+}
+
+// The powers of exp(*log_decay) that one thread of a table's takes.
+__device__ __forceinline__ void store_powers(float* table, const float* log_decay, int e) {
+  if (e > 128) return;
+  const double w = exp(static_cast<double>(usable_decay(__ldg(log_decay))) * e);
+  table[e] = static_cast<float>(w);
+  if (e == 128) table[129] = static_cast<float>(w - static_cast<float>(w));
+}
+
+// Four lanes with four 16-byte units each: afterwards unit k of lane g is
+// what unit g of lane k was.
+__device__ __forceinline__ void transpose4(uint32_t (&z)[16], int lane) {
+#pragma unroll
+  for (int m = 1; m <= 2; m *= 2) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (u & m) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t &lo = z[u * 4 + i], &hi = z[(u + m) * 4 + i];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, m);
+        if (up) lo = got; else hi = got;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
                                           volatile uint32_t* abort_flag, uint32_t* sticky) {
   const bool ok = mbar_wait(bar, parity, abort_flag, sticky);
@@ -113,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     scan_tc_kernel(const __grid_constant__ ScanMaps maps, const __grid_constant__ ScanArgs t) {
   using Pl = TcPlan<DA, DC>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ uint32_t check_flags;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (blockIdx.x == 0 && tid == 0) {
@@ -122,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  if (t.check && blockIdx.x == 0) check_inputs(t.s, &check_flags);
+  if (t.check && blockIdx.x == 0) check_inputs(t.s, reinterpret_cast<uint32_t*>(smem));
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Pl::kBars);
   uint64_t* full = bars;                   // [2] a stage's tiles have landed
@@ -136,9 +172,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* b_ready = bars + 16;           // w b stored
   uint64_t* o_full = bars + 17;            // M3 done (and M2)
   uint64_t* d_full = bars + 18;            // M4 done
-  uint64_t* tab_ready = bars + 19;         // a table of powers stored
-  uint64_t* drain = bars + 20;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  uint64_t* o_read = bars + 19;            // O1, O2 read
+  uint64_t* tab_ready = bars + 20;         // [2] a table of powers stored (state, output warps)
+  uint64_t* drain = bars + 22;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -147,16 +184,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, 9);
+      mbar_init(item_empty + i, STATE ? 9 : 13);
     }
     mbar_init(p_full, 1);
     mbar_init(s_ready, 8);
     mbar_init(a_free, 1);
-    mbar_init(p_ready, 8);
+    mbar_init(p_ready, 4);
     mbar_init(b_ready, 8);
     mbar_init(o_full, 1);
     mbar_init(d_full, 1);
+    mbar_init(o_read, 4);
     mbar_init(tab_ready, 8);
+    mbar_init(tab_ready + 1, 4);
     mbar_init(drain, 1);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -274,7 +313,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (lane == 0) m1(n);
           }
-          if (!warp_wait(s_ready, ph, abort_flag, sticky)) { ok = false; break; }
+          if (!warp_wait(s_ready, ph, abort_flag, sticky) ||
+              (n > 0 && !warp_wait(o_read, (n - 1) & 1u, abort_flag, sticky))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           if (lane == 0) {
             const uint64_t da = smem_desc(d + Pl::kA, 16, 1024, 2);
@@ -290,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ts(tmem + kColO1, tmem + kColP + (ks >> 2) * 64 + (ks & 3) * 8,
+              mma_bf16_ts(tmem + kColO1, tmem + kColP + ks * 8,
                           cm + ((ks * 2048) >> 4), id_o, ks > 0 ? 1u : 0u);
             mma_commit(o_full);
           }
@@ -333,17 +376,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(drain);
       mbar_wait_bounded(drain, 0);
     }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ decay, state, output
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------ state
     bool ok = true;
     const int q = warp & 3, hf = (warp - 4) >> 2, ctid = tid - 128;
-    const int row = q * 32 + lane;  // TMEM lane: row of the chunk, row of the state
+    const int row = q * 32 + lane;  // TMEM lane: row of the state
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    uint32_t tab = sbase + Pl::kTab, items = 0;
+    uint32_t tab = 0, items = 0, n = 0;
     constexpr int HC = DC / 2;
     const bool state_row = DA == 128 || q < 2;
-    float S[HC];
-    uint32_t n = 0;
+    uint64_t S[HC / 2];  // pairs of columns
     ScanItem it;
     auto power = [&](int e) { return ld_shared_f32(tab + e * 4); };
     // S <- (f + fl) S + D, once M4 of the chunk before is done.
@@ -354,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       if (state_row) {
+        const uint64_t f2 = f2_pack(f, f), fl2 = f2_pack(fl, fl);
 #pragma unroll
         for (int j = 0; j < HC / 32; ++j) {
           uint32_t v[32];
@@ -361,8 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           tmem_pin32(v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            S[j * 32 + e] = fmaf(f, S[j * 32 + e], fmaf(fl, S[j * 32 + e], __uint_as_float(v[e])));
+          for (int e = 0; e < 16; ++e)
+            S[j * 16 + e] = f2_fma(f2, S[j * 16 + e],
+                                   f2_fma(fl2, S[j * 16 + e],
+                                          f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]))));
         }
       }
       tc_fence_before();
@@ -373,35 +418,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The decay's powers, in one of two tables: a warp that writes a table
       // has seen tab_ready of the item before, so every warp has left the
       // item before that one, which used the same table.
-      const double g = static_cast<double>(usable_decay(__ldg(t.s.log_decay + it.head)));
       tab = sbase + Pl::kTab + (items & 1u) * (kTable * 4);
-      float* table = reinterpret_cast<float*>(smem + Pl::kTab) + (items & 1u) * kTable;
-      if (ctid <= 128) {
-        const double w = exp(g * ctid);
-        table[ctid] = static_cast<float>(w);
-        if (ctid == 128) table[129] = static_cast<float>(w - static_cast<float>(w));
-      }
+      store_powers(reinterpret_cast<float*>(smem + Pl::kTab) + (items & 1u) * kTable,
+                   t.s.log_decay + it.head, ctid);
       warp_arrive(tab_ready, lane);
       // The state to start from.
       if (state_row) {
         const bool seg = !STATE && it.from >= 0;
         const float* src = STATE ? nullptr : seg ? p.bound : p.ends;
         const float m = seg ? 1.f : p.ends_mul;
-        const bool tr = p.transposed != 0;
         const int64_t o = (seg ? it.from : it.state) * (DA * DC);
+        const int step = p.transposed ? DA : 1;
+        const int64_t first = o + (p.transposed ? row + hf * HC * DA : row * DC + hf * HC);
 #pragma unroll
-        for (int j = 0; j < HC; ++j) {
-          const int col = hf * HC + j;
-          S[j] = src == nullptr ? 0.f : m * src[o + (tr ? col * DA + row : row * DC + col)];
-        }
+        for (int j = 0; j < HC / 2; ++j)
+          S[j] = src == nullptr ? 0ull
+                                : f2_pack(m * src[first + (2 * j) * step], m * src[first + (2 * j + 1) * step]);
       }
       if (!warp_wait(tab_ready, items & 1u, abort_flag, sticky)) break;
       ++items;
       const int64_t chunks = (it.hi - it.lo + 127) / 128;
       float f = 0.f, fl = 0.f;  // decay of S over the chunk before
-      for (int64_t c = 0; c < chunks && ok; ++c, ++n) {
+      for (int64_t c = 0; c < chunks; ++c, ++n) {
         const uint32_t st = n % kStages, ph = n & 1u;
-        uint8_t* d = smem + st * Pl::kStage;
+        const uint32_t d = sbase + st * Pl::kStage;
         const int64_t r0 = it.lo + 128 * (rev ? chunks - 1 - c : c);
         const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
         // A reverse scan's first chunk of a user takes the start state undecayed.
@@ -415,88 +455,56 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int u = 0; u < HC / 8; ++u) {
             const int col = hf * HC + u * 8;
-            st_shared_v4(sbase + Pl::kS + (col >> 6) * Pl::kSBox + swz(row, (col & 63) >> 3),
-                         pack_bf16x2(S[u * 8], S[u * 8 + 1]), pack_bf16x2(S[u * 8 + 2], S[u * 8 + 3]),
-                         pack_bf16x2(S[u * 8 + 4], S[u * 8 + 5]),
-                         pack_bf16x2(S[u * 8 + 6], S[u * 8 + 7]));
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x, y;
+              f2_unpack(S[u * 4 + i], x, y);
+              w[i] = pack_bf16x2(x, y);
+            }
+            st_shared_v4(sbase + Pl::kS + (col >> 6) * Pl::kSBox + swz(row, (col & 63) >> 3), w[0], w[1],
+                         w[2], w[3]);
           }
         }
         if (!warp_wait(full + st, (n / kStages) & 1u, abort_flag, sticky)) { ok = false; break; }
         if (L < 128) {
           // Rows behind the end belong to another user or to nobody: c's must
           // not reach the sums, whatever they hold.
-          for (int e = ctid; e < (128 - L) * (DC / 8); e += kCompute) {
+          for (int e = ctid; e < (128 - L) * (DC / 8); e += kStateThreads) {
             const int r = L + e / (DC / 8), u = e % (DC / 8);
-            st_shared_v4(smem_u32(d) + Pl::kC + (u >> 3) * kBox + swz(r, u & 7), 0u, 0u, 0u, 0u);
+            st_shared_v4(d + Pl::kC + (u >> 3) * kBox + swz(r, u & 7), 0u, 0u, 0u, 0u);
           }
         }
         if (!STATE) {
           fence_proxy_async_smem();
           tc_fence_before();
           warp_arrive(s_ready, lane);
-          // s2: this half's 64 columns of P, 32 at a time.  A block of 32 x
-          // 32 that the scan covers whole has the weight E F_j, both powers
-          // with exponents >= 0; the one on the diagonal is masked.
-          if (!warp_wait(p_full, ph, abort_flag, sticky)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int jb = hf * 2 + k;
-            uint32_t o[16];
-            if (rev ? jb < q : jb > q) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = 0u;
-            } else {
-              uint32_t v[32];
-              tmem_ld32(lane_base + kColP + jb * 32, v);
-              tmem_wait_ld();
-              tmem_pin32(v);
-              if (jb == q) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const int dist = rev ? e - lane : lane - e;
-                  const bool in = dist >= 0 && jb * 32 + e < L;
-                  const float w = power(in ? dist : 0);
-                  v[e] = in ? __float_as_uint(__uint_as_float(v[e]) * w) : 0u;
-                }
-              } else {
-                const float E = power(rev ? jb * 32 - row : row - jb * 32 - 31);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const float w = E * power(rev ? e : 31 - e);
-                  v[e] = jb * 32 + e < L ? __float_as_uint(__uint_as_float(v[e]) * w) : 0u;
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                o[e] = pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-            }
-            tmem_st16(lane_base + kColP + hf * 64 + k * 16, o);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          warp_arrive(p_ready, lane);
           if (!warp_wait(a_free, ph, abort_flag, sticky)) { ok = false; break; }
         }
         // s3: w b in two or three bf16 parts, over b, over a and in S~'s place.
 #pragma unroll 4
-        for (int e = ctid; e < 128 * (DA / 8); e += kCompute) {
+        for (int e = ctid; e < 128 * (DA / 8); e += kStateThreads) {
           const int r = e / (DA / 8), u = e % (DA / 8);
           const uint32_t o = (u >> 3) * kBox + swz(r, u & 7);
-          const uint32_t src = smem_u32(d) + Pl::kB + o, dst = smem_u32(d) + Pl::kA + o;
-          uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u}, low[4] = {0u, 0u, 0u, 0u};
-          if (r < L) {
-            const float w = power(rev ? r : L - 1 - r);
-            const uint4 x = ld_shared_v4u(src);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t src = d + Pl::kB + o, dst = d + Pl::kA + o;
+          const float w1 = r < L ? power(rev ? r : L - 1 - r) : 0.f;
+          const uint64_t w = f2_pack(w1, w1), minus = f2_pack(-1.f, -1.f);
+          const uint4 x = ld_shared_v4u(src);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          uint32_t hi[4], lo[4], low[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float y0 = w * bf_lo(xs[i]), y1 = w * bf_hi(xs[i]);
-              hi[i] = pack_bf16x2(y0, y1);
-              y0 -= bf_lo(hi[i]), y1 -= bf_hi(hi[i]);
-              lo[i] = pack_bf16x2(y0, y1);
-              low[i] = pack_bf16x2(y0 - bf_lo(lo[i]), y1 - bf_hi(lo[i]));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v = r < L ? xs[i] : 0u;
+            uint64_t y = f2_mul(w, f2_pack(bf_lo(v), bf_hi(v)));
+            float y0, y1;
+            f2_unpack(y, y0, y1);
+            hi[i] = pack_bf16x2(y0, y1);
+            y = f2_fma(minus, f2_pack(bf_lo(hi[i]), bf_hi(hi[i])), y);
+            f2_unpack(y, y0, y1);
+            lo[i] = pack_bf16x2(y0, y1);
+            y = f2_fma(minus, f2_pack(bf_lo(lo[i]), bf_hi(lo[i])), y);
+            f2_unpack(y, y0, y1);
+            low[i] = pack_bf16x2(y0, y1);
           }
           st_shared_v4(src, hi[0], hi[1], hi[2], hi[3]);
           st_shared_v4(dst, lo[0], lo[1], lo[2], lo[3]);
@@ -504,47 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         warp_arrive(b_ready, lane);
-        // s4
-        if (!STATE) {
-          if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
-          tc_fence_after();
-          const float w = power(row < L ? (rev ? L - row : row + 1) - skip : 0);
-#pragma unroll
-          for (int j = 0; j < HC / 32; ++j) {
-            uint32_t x[32], y[32];
-            tmem_ld32(lane_base + kColO1 + hf * HC + j * 32, x);
-            tmem_ld32(lane_base + kColO2 + hf * HC + j * 32, y);
-            tmem_wait_ld();
-            tmem_pin32(x);
-            tmem_pin32(y);
-            if (row < L) {
-              float finite = 0.f;  // NaN if some O1 is not finite
-#pragma unroll
-              for (int e = 0; e < 32; ++e) finite = fmaf(__uint_as_float(x[e]), 0.f, finite);
-              if (finite != 0.f) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!isfinite(__uint_as_float(x[e])) && isfinite(__uint_as_float(y[e])))
-                    x[e] = __float_as_uint(masked_sum(p, it.head, r0, L, row, hf * HC + j * 32 + e, table));
-              }
-              uint4* o = reinterpret_cast<uint4*>(
-                  static_cast<uint16_t*>(p.out) + ((r0 + row) * t.s.heads + it.head) * DC + hf * HC + j * 32);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t z[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int k = e * 8 + i * 2;
-                  z[i] = pack_bf16x2(
-                      p.out_mul * fmaf(w, __uint_as_float(y[k]), __uint_as_float(x[k])),
-                      p.out_mul * fmaf(w, __uint_as_float(y[k + 1]), __uint_as_float(x[k + 1])));
-                }
-                o[e] = make_uint4(z[0], z[1], z[2], z[3]);
-              }
-            }
-          }
-          tc_fence_before();
-        }
       }
       if (!ok) break;
       if (chunks > 0) add_d(f, fl);
@@ -563,10 +530,147 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (dst != nullptr && state_row) {
 #pragma unroll
-        for (int j = 0; j < HC; j += 4)
-          *reinterpret_cast<float4*>(dst + o + row * DC + hf * HC + j) =
-              make_float4(m * S[j], m * S[j + 1], m * S[j + 2], m * S[j + 3]);
+        for (int j = 0; j < HC / 4; ++j) {
+          float4 v;
+          f2_unpack(S[2 * j], v.x, v.y);
+          f2_unpack(S[2 * j + 1], v.z, v.w);
+          v.x *= m, v.y *= m, v.z *= m, v.w *= m;
+          *reinterpret_cast<float4*>(dst + o + row * DC + hf * HC + j * 4) = v;
+        }
       }
+    }
+  } else if (!STATE && warp >= 12) {
+    // ------------------------------------------------------------ output
+    bool ok = true;
+    const int q = warp & 3, ctid = tid - 384;
+    const int row = q * 32 + lane;  // TMEM lane: row of the chunk
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t items = 0, n = 0;
+    ScanItem it;
+    while (take(it, ok)) {
+      const ScanPass& p = t.p[it.pass];
+      const bool rev = p.reverse != 0;
+      const uint32_t tab = sbase + Pl::kTab + (2 + (items & 1u)) * (kTable * 4);
+      float* table = reinterpret_cast<float*>(smem + Pl::kTab) + (2 + (items & 1u)) * kTable;
+      auto power = [&](int e) { return ld_shared_f32(tab + e * 4); };
+      store_powers(table, t.s.log_decay + it.head, ctid);
+      if (ctid == 0) store_powers(table, t.s.log_decay + it.head, 128);
+      warp_arrive(tab_ready + 1, lane);
+      if (!warp_wait(tab_ready + 1, items & 1u, abort_flag, sticky)) break;
+      ++items;
+      const int64_t chunks = (it.hi - it.lo + 127) / 128;
+      for (int64_t c = 0; c < chunks; ++c, ++n) {
+        const uint32_t ph = n & 1u;
+        const int64_t r0 = it.lo + 128 * (rev ? chunks - 1 - c : c);
+        const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
+        const int skip = rev && it.first && c == 0 ? 1 : 0;
+        // s2: 32 columns of P at a time; their 16 columns of P~ go where
+        // columns lay that have been read.  A block of 32 x 32 that the scan
+        // covers whole has the weight E F_j, both powers with exponents >= 0;
+        // the one on the diagonal is masked.
+        if (!warp_wait(p_full, ph, abort_flag, sticky)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll 1
+        for (int jb = 0; jb < 4; ++jb) {
+          uint32_t o[16];
+          if (rev ? jb < q : jb > q) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0u;
+          } else {
+            uint32_t v[32];
+            tmem_ld32(lane_base + kColP + jb * 32, v);
+            tmem_wait_ld();
+            tmem_pin32(v);
+            if (jb == q) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int dist = rev ? e - lane : lane - e;
+                const float w = power(dist >= 0 ? dist : 0);
+                v[e] = dist >= 0 ? __float_as_uint(__uint_as_float(v[e]) * w) : 0u;
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+            } else {
+              const float E1 = power(rev ? jb * 32 - row : row - jb * 32 - 31);
+              const uint64_t E = f2_pack(E1, E1);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint64_t w = f2_mul(E, f2_pack(power(rev ? 2 * e : 31 - 2 * e),
+                                                     power(rev ? 2 * e + 1 : 30 - 2 * e)));
+                float x, y;
+                f2_unpack(f2_mul(w, f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]))),
+                          x, y);
+                o[e] = pack_bf16x2(x, y);
+              }
+            }
+            if (L < jb * 32 + 32) {
+              // Columns behind the user's end.
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] &= (jb * 32 + 2 * e < L ? 0xFFFFu : 0u) | (jb * 32 + 2 * e + 1 < L ? 0xFFFF0000u : 0u);
+            }
+          }
+          tmem_st16(lane_base + kColP + jb * 16, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(p_ready, lane);
+        // s4
+        if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
+        tc_fence_after();
+        const float w1 = p.out_mul * power(row < L ? (rev ? L - row : row + 1) - skip : 0);
+        const uint64_t w = f2_pack(w1, w1), mul = f2_pack(p.out_mul, p.out_mul);
+#pragma unroll 1
+        for (int j = 0; j < DC / 32; ++j) {
+          uint32_t x[32], y[32], z[16];
+          tmem_ld32(lane_base + kColO1 + j * 32, x);
+          tmem_ld32(lane_base + kColO2 + j * 32, y);
+          tmem_wait_ld();
+          tmem_pin32(x);
+          tmem_pin32(y);
+          uint64_t finite = 0ull;  // NaN if some O1 is not finite
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t x2 = f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+            const uint64_t y2 = f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+            finite = f2_fma(x2, 0ull, finite);
+            float u, v;
+            f2_unpack(f2_fma(w, y2, f2_mul(mul, x2)), u, v);
+            z[e] = pack_bf16x2(u, v);
+          }
+          float f0, f1;
+          f2_unpack(finite, f0, f1);
+          if (__any_sync(0xFFFFFFFFu, (f0 != 0.f || f1 != 0.f) && row < L)) {
+#pragma unroll 1
+            for (int e = 0; e < 32; ++e) {
+              uint32_t own, share;
+              tmem_ld1(lane_base + kColO1 + j * 32 + e, own);
+              tmem_ld1(lane_base + kColO2 + j * 32 + e, share);
+              tmem_wait_ld();
+              tmem_pin1(own);
+              tmem_pin1(share);
+              if (row < L && !isfinite(__uint_as_float(own)) && isfinite(__uint_as_float(share)))
+                put_half(z, e, fmaf(w1, __uint_as_float(share),
+                                    p.out_mul * masked_sum(p, it.head, r0, L, row, j * 32 + e, table)));
+              __syncwarp();
+            }
+          }
+          // A thread holds 64 bytes of its row; four threads exchange them so
+          // that a store's four lanes cover 64 bytes of one row together.
+          transpose4(z, lane);
+          uint16_t* o = static_cast<uint16_t*>(p.out) +
+                        ((r0 + (row & ~3)) * t.s.heads + it.head) * DC + j * 32 + (lane & 3) * 8;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((row & ~3) + k < L)
+              *reinterpret_cast<uint4*>(o + static_cast<int64_t>(k) * t.s.heads * DC) =
+                  make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
+        }
+        tc_fence_before();
+        warp_arrive(o_read, lane);
+      }
+      if (!ok) break;
     }
   }
   tc_fence_before();
