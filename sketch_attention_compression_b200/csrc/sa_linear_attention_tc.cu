@@ -20,13 +20,12 @@
 // two stages), warp 1 issues the MMAs.  Warps 4-11 hold the state, two warps
 // per TMEM lane quarter, each with half of the columns; per chunk they
 //   s1  add D of the chunk before to S and store S~
-//   s3  split w b into the stage's own b and a tiles (M1 and M2 have read
-//       them) and S~'s place
-// and warps 12-15 make the output, one row of the chunk per thread:
-//   s2  turn P into P~ (TMEM to TMEM)
-//   s4  store out, while M4 and the next chunk's M1 run.
-// The chain s1, M2, s3, M4 carries the state from chunk to chunk; s2, M3 and
-// s4 run beside it.
+//   s3  split w b: the first part over b, which M1 has read, the others in
+//       places of their own (da = 64), or over a and in S~'s place once M2
+//       has read those
+//   s4  store out, while M4 runs
+// and warps 12-15 turn P into P~ (s2, TMEM to TMEM), one row per thread,
+// while M2 and s3 run.
 // TMEM: P and P~ at 0, O1 at 128, O2 at 256, D at 384.  Shared memory at
 // da = dc = 128: two stages of three 32 KB tiles and 32 KB for S~: 224 KB.
 //
@@ -57,19 +56,30 @@ struct TcPlan {
   static constexpr int kStage = kC + (DC / 64) * kBox;
   static constexpr int kS = kStages * kStage;           // S~: dc / 64 boxes of da rows
   static constexpr int kSBox = DA * 128;
-  static constexpr int kTab = kS + 2 * kBox;            // four tables of the decay's powers
+  // The low parts of w b.  da = 64: one place per stage for each, and 16 KB
+  // behind them that M4 reads; else over a and in S~'s place.
+  static constexpr bool kOwn = DA == 64;
+  static constexpr int kLow = kS + (DC / 64) * kSBox;
+  static constexpr int kTab = kOwn ? kLow + 5 * kBox : kS + 2 * kBox;  // four tables of powers
   static constexpr int kItems = kTab + 4 * kTable * 4;
   static constexpr int kBars = kItems + kRing * 64;
   // M4 with da = 64 reads a second box behind each part that is not the
   // part's: those rows of D are never used, and the reads stay inside the
-  // stages and S~'s two boxes.
+  // allocation.
   static constexpr int kUsed = kBars + 256;
   // At least 116 KB, so that one CTA holds an SM (it allocates all of TMEM).
   static constexpr int kSmem = kUsed > 118784 ? kUsed : 118784;
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kItems % 16 == 0 && kBars % 8 == 0, "alignment");
   static_assert(kB + 2 * kBox <= kStage, "second box of b inside its stage");
-  static_assert((DC / 64) * kSBox <= 2 * kBox, "S~ in its place");
+  static_assert(kOwn || (DC / 64) * kSBox <= 2 * kBox, "S~ in its place");
+  // Shared-memory offsets of the second and third part of stage st's w b.
+  static __device__ __forceinline__ int part2(uint32_t st) {
+    return kOwn ? kLow + static_cast<int>(st) * kBox : static_cast<int>(st) * kStage + kA;
+  }
+  static __device__ __forceinline__ int part3(uint32_t st) {
+    return kOwn ? kLow + (2 + static_cast<int>(st)) * kBox : kS;
+  }
 };
 
 static_assert(sizeof(ScanItem) <= 64, "ring entry");
@@ -85,26 +95,21 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 
 // O1 of one output, over the rows that the scan has reached: for outputs that
 // values behind the mask have spoiled.
-__device__ __noinline__ float masked_sum(const ScanPass& p, int head, int64_t r0, int L, int i,
-                                         int col, const float* power) {
+__device__ __forceinline__ float masked_sum(const ScanPass& p, int head, int64_t r0, int L, int i,
+                                            int col, uint32_t powers) {
   auto at = [&](const ScanInput& in, int r, int c) {
     return bf_lo(static_cast<const uint16_t*>(
         in.p)[(r0 + r) * in.row + static_cast<int64_t>(head) * in.head + c]);
   };
   float sum = 0.f;
+#pragma unroll 1
   for (int j = p.reverse ? i : 0; j < (p.reverse ? L : i + 1); ++j) {
     float x = 0.f;
+#pragma unroll 1
     for (int d = 0; d < p.da; ++d) x = fmaf(at(p.a, i, d), at(p.b, j, d), x);
-    sum = fmaf(x * power[p.reverse ? j - i : i - j], at(p.c, j, col), sum);
+    sum = fmaf(x * ld_shared_f32(powers + (p.reverse ? j - i : i - j) * 4), at(p.c, j, col), sum);
   }
   return sum;
-}
-
-// Element e of packed pairs becomes x.
-__device__ __forceinline__ void put_half(uint32_t (&z)[16], int e, float x) {
-  const uint32_t w = pack_bf16x2(x, x), mask = e & 1 ? 0xFFFF0000u : 0xFFFFu;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] = e / 2 == i ? (z[i] & ~mask) | (w & mask) : z[i];
 }
 
 // The powers of exp(*log_decay) that one thread of a table's takes.
@@ -113,25 +118,6 @@ __device__ __forceinline__ void store_powers(float* table, const float* log_deca
   const double w = exp(static_cast<double>(usable_decay(__ldg(log_decay))) * e);
   table[e] = static_cast<float>(w);
   if (e == 128) table[129] = static_cast<float>(w - static_cast<float>(w));
-}
-
-// Four lanes with four 16-byte units each: afterwards unit k of lane g is
-// what unit g of lane k was.
-__device__ __forceinline__ void transpose4(uint32_t (&z)[16], int lane) {
-#pragma unroll
-  for (int m = 1; m <= 2; m *= 2) {
-    const bool up = (lane & m) != 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (u & m) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t &lo = z[u * 4 + i], &hi = z[(u + m) * 4 + i];
-        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, m);
-        if (up) lo = got; else hi = got;
-      }
-    }
-  }
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
@@ -143,6 +129,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
+  __syncwarp();  // the other lanes' next wait must not hold the arrival up
 }
 
 template <int DA, int DC, bool STATE>
@@ -172,10 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* b_ready = bars + 16;           // w b stored
   uint64_t* o_full = bars + 17;            // M3 done (and M2)
   uint64_t* d_full = bars + 18;            // M4 done
-  uint64_t* o_read = bars + 19;            // O1, O2 read
-  uint64_t* tab_ready = bars + 20;         // [2] a table of powers stored (state, output warps)
-  uint64_t* drain = bars + 22;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
+  uint64_t* tab_ready = bars + 19;         // [2] a table of powers stored (state, weight warps)
+  uint64_t* drain = bars + 21;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -193,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(b_ready, 8);
     mbar_init(o_full, 1);
     mbar_init(d_full, 1);
-    mbar_init(o_read, 4);
     mbar_init(tab_ready, 8);
     mbar_init(tab_ready + 1, 4);
     mbar_init(drain, 1);
@@ -288,14 +273,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_o = idesc_bf16_f32(128, DC, 0, 1);
     constexpr uint32_t id_d = idesc_bf16_f32(128, DC, 1, 1);
     uint32_t n = 0;
+    // Every lane waits for the issuing one: lanes that ran ahead would poll
+    // the next barrier in turns with its instructions.  Products are issued
+    // in groups of four steps of K (64 columns of a K-major operand, 64 rows
+    // of an MN-major one).
+    auto group = [&](uint32_t acc, uint64_t da, int step_a, uint64_t db, int step_b, uint32_t id,
+                     bool first) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        mma_bf16_ss(acc, da + i * step_a, db + i * step_b, id, first && i == 0 ? 0u : 1u);
+    };
+    constexpr int kStepK = 32 >> 4, kStepMn = 2048 >> 4;
     auto m1 = [&](uint32_t c) {
       const uint32_t d = sbase + (c % kStages) * Pl::kStage;
       const uint64_t da = smem_desc(d + Pl::kA, 16, 1024, 2), db = smem_desc(d + Pl::kB, 16, 1024, 2);
 #pragma unroll
-      for (int ks = 0; ks < DA / 16; ++ks) {
-        const uint64_t o = ((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
-        mma_bf16_ss(tmem + kColP, da + o, db + o, id_p, ks > 0 ? 1u : 0u);
-      }
+      for (int g = 0; g < DA / 64; ++g)
+        group(tmem + kColP, da + g * (kBox >> 4), kStepK, db + g * (kBox >> 4), kStepK, id_p, g == 0);
       mma_commit(p_full);
     };
     ScanItem it;
@@ -312,31 +306,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(full + st, (n / kStages) & 1u, abort_flag, sticky)) { ok = false; break; }
             tc_fence_after();
             if (lane == 0) m1(n);
+            __syncwarp();
           }
-          if (!warp_wait(s_ready, ph, abort_flag, sticky) ||
-              (n > 0 && !warp_wait(o_read, (n - 1) & 1u, abort_flag, sticky))) {
-            ok = false;
-            break;
-          }
+          if (!warp_wait(s_ready, ph, abort_flag, sticky)) { ok = false; break; }
           tc_fence_after();
           if (lane == 0) {
             const uint64_t da = smem_desc(d + Pl::kA, 16, 1024, 2);
             const uint64_t sm = smem_desc(sbase + Pl::kS, Pl::kSBox, 1024, 2);
 #pragma unroll
-            for (int ks = 0; ks < DA / 16; ++ks)
-              mma_bf16_ss(tmem + kColO2, da + (((ks >> 2) * kBox + (ks & 3) * 32) >> 4),
-                          sm + ((ks * 2048) >> 4), id_o, ks > 0 ? 1u : 0u);
+            for (int g = 0; g < DA / 64; ++g)
+              group(tmem + kColO2, da + g * (kBox >> 4), kStepK, sm + g * 4 * kStepMn, kStepMn, id_o, g == 0);
             mma_commit(a_free);
           }
+          __syncwarp();
           if (!warp_wait(p_ready, ph, abort_flag, sticky)) { ok = false; break; }
           tc_fence_after();
           if (lane == 0) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ts(tmem + kColO1, tmem + kColP + ks * 8,
-                          cm + ((ks * 2048) >> 4), id_o, ks > 0 ? 1u : 0u);
+            for (int g = 0; g < 2; ++g) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_bf16_ts(tmem + kColO1, tmem + kColP + (g * 4 + i) * 8, cm + (g * 4 + i) * kStepMn, id_o,
+                            g + i > 0 ? 1u : 0u);
+            }
             mma_commit(o_full);
           }
+          __syncwarp();
           // The next chunk's M1 goes before this chunk's M4 if its tiles are there.
           if (c + 1 < chunks) {
             next = __all_sync(0xFFFFFFFFu,
@@ -344,26 +339,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (next) {
               tc_fence_after();
               if (lane == 0) m1(n + 1);
+              __syncwarp();
             }
           }
         }
         if (!warp_wait(b_ready, ph, abort_flag, sticky)) { ok = false; break; }
         tc_fence_after();
         if (lane == 0) {
-          const uint64_t hi = smem_desc(d + Pl::kB, kBox, 1024, 2);  // w b, MN-major A
-          const uint64_t lo = smem_desc(d + Pl::kA, kBox, 1024, 2);
+          // w b, MN-major A
+          const uint64_t hi = smem_desc(d + Pl::kB, kBox, 1024, 2);
+          const uint64_t lo = smem_desc(sbase + Pl::part2(st), kBox, 1024, 2);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ss(tmem + kColD, hi + ((ks * 2048) >> 4), cm + ((ks * 2048) >> 4), id_d,
-                        ks > 0 ? 1u : 0u);
+          for (int g = 0; g < 2; ++g)
+            group(tmem + kColD, hi + g * 4 * kStepMn, kStepMn, cm + g * 4 * kStepMn, kStepMn, id_d, g == 0);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ss(tmem + kColD, lo + ((ks * 2048) >> 4), cm + ((ks * 2048) >> 4), id_d, 1u);
+          for (int g = 0; g < 2; ++g)
+            group(tmem + kColD, lo + g * 4 * kStepMn, kStepMn, cm + g * 4 * kStepMn, kStepMn, id_d, false);
           if (t.p[it.pass].parts == 3) {
-            const uint64_t low = smem_desc(sbase + Pl::kS, kBox, 1024, 2);
+            const uint64_t low = smem_desc(sbase + Pl::part3(st), kBox, 1024, 2);
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ss(tmem + kColD, low + ((ks * 2048) >> 4), cm + ((ks * 2048) >> 4), id_d, 1u);
+            for (int g = 0; g < 2; ++g)
+              group(tmem + kColD, low + g * 4 * kStepMn, kStepMn, cm + g * 4 * kStepMn, kStepMn, id_d, false);
           }
           mma_commit(empty + st);
           mma_commit(d_full);
@@ -398,16 +394,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (state_row) {
         const uint64_t f2 = f2_pack(f, f), fl2 = f2_pack(fl, fl);
 #pragma unroll
-        for (int j = 0; j < HC / 32; ++j) {
-          uint32_t v[32];
-          tmem_ld32(lane_base + kColD + hf * HC + j * 32, v);
+        for (int j = 0; j < HC / 16; ++j) {
+          uint32_t v[16];
+          tmem_ld16(lane_base + kColD + hf * HC + j * 16, v);
           tmem_wait_ld();
-          tmem_pin32(v);
+          tmem_pin16(v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            S[j * 16 + e] = f2_fma(f2, S[j * 16 + e],
-                                   f2_fma(fl2, S[j * 16 + e],
-                                          f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]))));
+          for (int e = 0; e < 8; ++e)
+            S[j * 8 + e] = f2_fma(f2, S[j * 8 + e],
+                                  f2_fma(fl2, S[j * 8 + e],
+                                         f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]))));
         }
       }
       tc_fence_before();
@@ -439,6 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
       const int64_t chunks = (it.hi - it.lo + 127) / 128;
       float f = 0.f, fl = 0.f;  // decay of S over the chunk before
+      // s3 is early where its places do not depend on M2.
+      const bool early = Pl::kOwn || (STATE && p.parts == 2);
       for (int64_t c = 0; c < chunks; ++c, ++n) {
         const uint32_t st = n % kStages, ph = n & 1u;
         const uint32_t d = sbase + st * Pl::kStage;
@@ -446,26 +444,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
         // A reverse scan's first chunk of a user takes the start state undecayed.
         const int skip = rev && it.first && c == 0 ? 1 : 0;
-        // s1
-        if (c > 0) add_d(f, fl);
-        if (!ok) break;
-        f = power(L - skip);
-        fl = L - skip == 128 ? power(129) : 0.f;
-        if (!STATE && state_row) {
-#pragma unroll
-          for (int u = 0; u < HC / 8; ++u) {
-            const int col = hf * HC + u * 8;
-            uint32_t w[4];
+        // s3: w b in two or three bf16 parts, the first one over b.
+        auto split = [&]() {
+#pragma unroll 2
+          for (int e = ctid; e < 128 * (DA / 8); e += kStateThreads) {
+            const int r = e / (DA / 8), u = e % (DA / 8);
+            const uint32_t o = (u >> 3) * kBox + swz(r, u & 7), src = d + Pl::kB + o;
+            const float w1 = r < L ? power(rev ? r : L - 1 - r) : 0.f;
+            const uint64_t w = f2_pack(w1, w1), minus = f2_pack(-1.f, -1.f);
+            const uint4 x = ld_shared_v4u(src);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            uint32_t hi[4], lo[4], low[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float x, y;
-              f2_unpack(S[u * 4 + i], x, y);
-              w[i] = pack_bf16x2(x, y);
+              const uint32_t v = r < L ? xs[i] : 0u;
+              uint64_t y = f2_mul(w, f2_pack(bf_lo(v), bf_hi(v)));
+              float y0, y1;
+              f2_unpack(y, y0, y1);
+              hi[i] = pack_bf16x2(y0, y1);
+              y = f2_fma(minus, f2_pack(bf_lo(hi[i]), bf_hi(hi[i])), y);
+              f2_unpack(y, y0, y1);
+              lo[i] = pack_bf16x2(y0, y1);
+              y = f2_fma(minus, f2_pack(bf_lo(lo[i]), bf_hi(lo[i])), y);
+              f2_unpack(y, y0, y1);
+              low[i] = pack_bf16x2(y0, y1);
             }
-            st_shared_v4(sbase + Pl::kS + (col >> 6) * Pl::kSBox + swz(row, (col & 63) >> 3), w[0], w[1],
-                         w[2], w[3]);
+            st_shared_v4(src, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(sbase + Pl::part2(st) + o, lo[0], lo[1], lo[2], lo[3]);
+            if (p.parts == 3) st_shared_v4(sbase + Pl::part3(st) + o, low[0], low[1], low[2], low[3]);
           }
-        }
+        };
         if (!warp_wait(full + st, (n / kStages) & 1u, abort_flag, sticky)) { ok = false; break; }
         if (L < 128) {
           // Rows behind the end belong to another user or to nobody: c's must
@@ -475,43 +483,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v4(d + Pl::kC + (u >> 3) * kBox + swz(r, u & 7), 0u, 0u, 0u, 0u);
           }
         }
+        if (early) {
+          if (!STATE && !warp_wait(p_full, ph, abort_flag, sticky)) { ok = false; break; }
+          split();
+        }
+        // s1
+        if (c > 0) add_d(f, fl);
+        if (!ok) break;
+        f = power(L - skip);
+        fl = L - skip == 128 ? power(129) : 0.f;
         if (!STATE) {
+          if (state_row) {
+#pragma unroll
+            for (int u = 0; u < HC / 8; ++u) {
+              const int col = hf * HC + u * 8;
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float x, y;
+                f2_unpack(S[u * 4 + i], x, y);
+                w[i] = pack_bf16x2(x, y);
+              }
+              st_shared_v4(sbase + Pl::kS + (col >> 6) * Pl::kSBox + swz(row, (col & 63) >> 3), w[0], w[1],
+                           w[2], w[3]);
+            }
+          }
           fence_proxy_async_smem();
           tc_fence_before();
           warp_arrive(s_ready, lane);
-          if (!warp_wait(a_free, ph, abort_flag, sticky)) { ok = false; break; }
         }
-        // s3: w b in two or three bf16 parts, over b, over a and in S~'s place.
-#pragma unroll 4
-        for (int e = ctid; e < 128 * (DA / 8); e += kStateThreads) {
-          const int r = e / (DA / 8), u = e % (DA / 8);
-          const uint32_t o = (u >> 3) * kBox + swz(r, u & 7);
-          const uint32_t src = d + Pl::kB + o, dst = d + Pl::kA + o;
-          const float w1 = r < L ? power(rev ? r : L - 1 - r) : 0.f;
-          const uint64_t w = f2_pack(w1, w1), minus = f2_pack(-1.f, -1.f);
-          const uint4 x = ld_shared_v4u(src);
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-          uint32_t hi[4], lo[4], low[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t v = r < L ? xs[i] : 0u;
-            uint64_t y = f2_mul(w, f2_pack(bf_lo(v), bf_hi(v)));
-            float y0, y1;
-            f2_unpack(y, y0, y1);
-            hi[i] = pack_bf16x2(y0, y1);
-            y = f2_fma(minus, f2_pack(bf_lo(hi[i]), bf_hi(hi[i])), y);
-            f2_unpack(y, y0, y1);
-            lo[i] = pack_bf16x2(y0, y1);
-            y = f2_fma(minus, f2_pack(bf_lo(lo[i]), bf_hi(lo[i])), y);
-            f2_unpack(y, y0, y1);
-            low[i] = pack_bf16x2(y0, y1);
-          }
-          st_shared_v4(src, hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(dst, lo[0], lo[1], lo[2], lo[3]);
-          if (p.parts == 3) st_shared_v4(sbase + Pl::kS + o, low[0], low[1], low[2], low[3]);
+        if (!early) {
+          if (!STATE && !warp_wait(a_free, ph, abort_flag, sticky)) { ok = false; break; }
+          split();
         }
         fence_proxy_async_smem();
         warp_arrive(b_ready, lane);
+        // s4
+        if (!STATE) {
+          if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
+          tc_fence_after();
+          const float w1 = p.out_mul * power(row < L ? (rev ? L - row : row + 1) - skip : 0);
+          const uint64_t w2 = f2_pack(w1, w1), mul = f2_pack(p.out_mul, p.out_mul);
+#pragma unroll 1
+          for (int col = hf * HC; col < hf * HC + HC; col += 16) {
+            uint32_t x1[16], y[16], z[8];
+            tmem_ld16(lane_base + kColO1 + col, x1);
+            tmem_ld16(lane_base + kColO2 + col, y);
+            tmem_wait_ld();
+            tmem_pin16(x1);
+            tmem_pin16(y);
+            uint64_t finite = 0ull;  // NaN if some O1 is not finite
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint64_t x2 = f2_pack(__uint_as_float(x1[2 * e]), __uint_as_float(x1[2 * e + 1]));
+              const uint64_t y2 = f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+              finite = f2_fma(x2, 0ull, finite);
+              float u, v;
+              f2_unpack(f2_fma(w2, y2, f2_mul(mul, x2)), u, v);
+              z[e] = pack_bf16x2(u, v);
+            }
+            float f0, f1;
+            f2_unpack(finite, f0, f1);
+            // A thread holds 32 bytes of its row; two threads exchange halves
+            // so that their stores cover 32 bytes of one row together.
+            const bool odd = (lane & 1) != 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? z[i] : z[i + 4], 1);
+              if (odd) z[i] = got; else z[i + 4] = got;
+            }
+            uint16_t* o = static_cast<uint16_t*>(p.out) +
+                          ((r0 + (row & ~1)) * t.s.heads + it.head) * DC + col + (odd ? 8 : 0);
+            if ((row & ~1) < L) *reinterpret_cast<uint4*>(o) = make_uint4(z[0], z[1], z[2], z[3]);
+            if ((row | 1) < L)
+              *reinterpret_cast<uint4*>(o + static_cast<int64_t>(t.s.heads) * DC) =
+                  make_uint4(z[4], z[5], z[6], z[7]);
+            if (__any_sync(0xFFFFFFFFu, f0 != 0.f || f1 != 0.f)) {
+              uint16_t* own_row = static_cast<uint16_t*>(p.out) +
+                                  ((r0 + row) * t.s.heads + it.head) * DC + col;
+#pragma unroll 1
+              for (int e = 0; e < 16; ++e) {
+                uint32_t own, share;
+                tmem_ld1(lane_base + kColO1 + col + e, own);
+                tmem_ld1(lane_base + kColO2 + col + e, share);
+                tmem_wait_ld();
+                tmem_pin1(own);
+                tmem_pin1(share);
+                if (row < L && !isfinite(__uint_as_float(own)) && isfinite(__uint_as_float(share)))
+                  own_row[e] = static_cast<uint16_t>(
+                      pack_bf16x2(fmaf(w1, __uint_as_float(share),
+                                       p.out_mul * masked_sum(p, it.head, r0, L, row, col + e, tab)),
+                                  0.f));
+                __syncwarp();
+              }
+            }
+          }
+          tc_fence_before();
+        }
       }
       if (!ok) break;
       if (chunks > 0) add_d(f, fl);
@@ -540,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (!STATE && warp >= 12) {
-    // ------------------------------------------------------------ output
+    // ------------------------------------------------------------ weights
     bool ok = true;
     const int q = warp & 3, ctid = tid - 384;
     const int row = q * 32 + lane;  // TMEM lane: row of the chunk
@@ -563,7 +631,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ph = n & 1u;
         const int64_t r0 = it.lo + 128 * (rev ? chunks - 1 - c : c);
         const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
-        const int skip = rev && it.first && c == 0 ? 1 : 0;
         // s2: 32 columns of P at a time; their 16 columns of P~ go where
         // columns lay that have been read.  A block of 32 x 32 that the scan
         // covers whole has the weight E F_j, both powers with exponents >= 0;
@@ -616,59 +683,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(p_ready, lane);
-        // s4
-        if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
-        tc_fence_after();
-        const float w1 = p.out_mul * power(row < L ? (rev ? L - row : row + 1) - skip : 0);
-        const uint64_t w = f2_pack(w1, w1), mul = f2_pack(p.out_mul, p.out_mul);
-#pragma unroll 1
-        for (int j = 0; j < DC / 32; ++j) {
-          uint32_t x[32], y[32], z[16];
-          tmem_ld32(lane_base + kColO1 + j * 32, x);
-          tmem_ld32(lane_base + kColO2 + j * 32, y);
-          tmem_wait_ld();
-          tmem_pin32(x);
-          tmem_pin32(y);
-          uint64_t finite = 0ull;  // NaN if some O1 is not finite
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t x2 = f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-            const uint64_t y2 = f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
-            finite = f2_fma(x2, 0ull, finite);
-            float u, v;
-            f2_unpack(f2_fma(w, y2, f2_mul(mul, x2)), u, v);
-            z[e] = pack_bf16x2(u, v);
-          }
-          float f0, f1;
-          f2_unpack(finite, f0, f1);
-          if (__any_sync(0xFFFFFFFFu, (f0 != 0.f || f1 != 0.f) && row < L)) {
-#pragma unroll 1
-            for (int e = 0; e < 32; ++e) {
-              uint32_t own, share;
-              tmem_ld1(lane_base + kColO1 + j * 32 + e, own);
-              tmem_ld1(lane_base + kColO2 + j * 32 + e, share);
-              tmem_wait_ld();
-              tmem_pin1(own);
-              tmem_pin1(share);
-              if (row < L && !isfinite(__uint_as_float(own)) && isfinite(__uint_as_float(share)))
-                put_half(z, e, fmaf(w1, __uint_as_float(share),
-                                    p.out_mul * masked_sum(p, it.head, r0, L, row, j * 32 + e, table)));
-              __syncwarp();
-            }
-          }
-          // A thread holds 64 bytes of its row; four threads exchange them so
-          // that a store's four lanes cover 64 bytes of one row together.
-          transpose4(z, lane);
-          uint16_t* o = static_cast<uint16_t*>(p.out) +
-                        ((r0 + (row & ~3)) * t.s.heads + it.head) * DC + j * 32 + (lane & 3) * 8;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if ((row & ~3) + k < L)
-              *reinterpret_cast<uint4*>(o + static_cast<int64_t>(k) * t.s.heads * DC) =
-                  make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
-        }
-        tc_fence_before();
-        warp_arrive(o_read, lane);
       }
       if (!ok) break;
     }
