@@ -2,15 +2,15 @@
 // The scans and their formulas are in sa_linear_attention.h.  Chunks have 128
 // rows; per chunk, with all operands in shared memory:
 //
-//   M1  P  = a b^T                    M 128, N 128, K da
-//       P~ = P weighted and masked    (bf16, TMEM)
-//   M2  O2 = a S~                     M 128, N dc,  K da   (S~: S in bf16)
-//   M3  O1 = P~ c                     M 128, N dc,  K 128  (A from TMEM)
-//   M4  D  = (w b)^T c                M da,  N dc,  K 128, w_j = l^(L-1-r_j)
-//       out = mul (O1 + l^(r+1) O2);  S <- l^L S + D
+//   M1  P   = a b^T                   M 128, N 128, K da
+//       P~  = mul P, weighted and masked   (bf16, TMEM)
+//   M2  O2  = a S~                    M 128, N dc,  K da   (S~: S in bf16)
+//   M3  O1  = P~ c                    M 128, N dc,  K 128  (A from TMEM)
+//   M4  D^T = c^T (w b)               M dc,  N da,  K 128, w_j = l^(L-1-r_j)
+//       out = O1 + mul l^(r+1) O2;  S <- l^L S + D
 //
 // Roundings to bf16: P~ and S~, the operands of an output that is bf16
-// itself.  S is kept in fp32 registers: w b is split into bf16 parts whose
+// itself.  S^T is kept in fp32 registers: w b is split into bf16 parts whose
 // products are all accumulated, three parts (24 significant bits) where the
 // state itself is an answer, two (16 bits) where only S~ is taken from it;
 // each chunk's D starts from zero and is added to S in registers, so that
@@ -23,10 +23,17 @@
 //   s3  split w b: the first part over b, which M1 has read, the others in
 //       places of their own (da = 64), or over a and in S~'s place once M2
 //       has read those
-//   s4  store out, while M4 runs
-// and warps 12-15 turn P into P~ (s2, TMEM to TMEM), one row per thread,
-// while M2 and s3 run.
-// TMEM: P and P~ at 0, O1 at 128, O2 at 256, D at 384.  Shared memory at
+//   s4  store most columns of out, while M4 runs
+// and warps 12-15, one row of the chunk per thread,
+//   s2  turn P into P~ (TMEM to TMEM), while M2 and s3 run
+//   s4  store the last 32 columns of out.
+// What bounds it: shared memory.  The products' operands, the split, the
+// state's copy and the loads move 560 KB per chunk at da = dc = 128, 4400
+// cycles at 128 bytes each, against 5500 cycles of its share of DRAM; the
+// rest of the time is the chain s1, M2, s3, M4.  With da = 64 the parts of
+// w b lie side by side, so that one product of N = 128 or 192 reads c once
+// for all of them.
+// TMEM: P and P~ at 0, O1 at 128, O2 at 256, D behind it.  Shared memory at
 // da = dc = 128: two stages of three 32 KB tiles and 32 KB for S~: 224 KB.
 //
 // A product of P~ = 0 with a c that is not finite is NaN, so a row could see
@@ -52,39 +59,31 @@ template <int DA, int DC>
 struct TcPlan {
   static constexpr int kA = 0;                          // within a stage
   static constexpr int kB = kA + (DA / 64) * kBox;
-  static constexpr int kC = kB + (DA / 64) * kBox;
-  static constexpr int kStage = kC + (DC / 64) * kBox;
-  static constexpr int kS = kStages * kStage;           // S~: dc / 64 boxes of da rows
-  static constexpr int kSBox = DA * 128;
-  // The low parts of w b.  da = 64: one place per stage for each, and 16 KB
-  // behind them that M4 reads; else over a and in S~'s place.
+  // The low parts of w b.  da = 64: boxes of their own behind b; else they
+  // lie over a and in S~'s place.
   static constexpr bool kOwn = DA == 64;
-  static constexpr int kLow = kS + (DC / 64) * kSBox;
-  static constexpr int kTab = kOwn ? kLow + 5 * kBox : kS + 2 * kBox;  // four tables of powers
+  static constexpr int kC = kB + (kOwn ? 3 : DA / 64) * kBox;
+  static constexpr int kStage = kC + (DC / 64) * kBox;
+  static constexpr int kS = kStages * kStage;           // S~^T: da / 64 boxes of dc rows
+  static constexpr int kSBox = DC * 128;
+  static constexpr int kTab = kS + (kOwn ? kSBox : 2 * kBox);  // four tables of powers
   static constexpr int kItems = kTab + 4 * kTable * 4;
   static constexpr int kBars = kItems + kRing * 64;
-  // M4 with da = 64 reads a second box behind each part that is not the
-  // part's: those rows of D are never used, and the reads stay inside the
-  // allocation.
   static constexpr int kUsed = kBars + 256;
-  // At least 116 KB, so that one CTA holds an SM (it allocates all of TMEM).
-  static constexpr int kSmem = kUsed > 118784 ? kUsed : 118784;
+  // M4 with dc = 64 reads a second box behind c's: those rows of D are never
+  // used, and the reads stay inside the allocation.  At least 116 KB, so
+  // that one CTA holds an SM (it allocates all of TMEM).
+  static constexpr int kNeed = kUsed > kS + kBox ? kUsed : kS + kBox;
+  static constexpr int kSmem = kNeed > 118784 ? kNeed : 118784;
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kItems % 16 == 0 && kBars % 8 == 0, "alignment");
-  static_assert(kB + 2 * kBox <= kStage, "second box of b inside its stage");
-  static_assert(kOwn || (DC / 64) * kSBox <= 2 * kBox, "S~ in its place");
-  // Shared-memory offsets of the second and third part of stage st's w b.
-  static __device__ __forceinline__ int part2(uint32_t st) {
-    return kOwn ? kLow + static_cast<int>(st) * kBox : static_cast<int>(st) * kStage + kA;
-  }
-  static __device__ __forceinline__ int part3(uint32_t st) {
-    return kOwn ? kLow + (2 + static_cast<int>(st)) * kBox : kS;
-  }
+  static constexpr int kColD = DC == 64 ? 320 : 384;
 };
 
 static_assert(sizeof(ScanItem) <= 64, "ring entry");
 
-constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256, kColD = 384;
+constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256;
+constexpr int kSideCols = 32;  // columns of out that warps 12-15 store
 
 __device__ __forceinline__ uint32_t swz(int r, int u) {
   return (r >> 3) * 1024 + (r & 7) * 128 + ((u ^ (r & 7)) << 4);
@@ -132,6 +131,66 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();  // the other lanes' next wait must not hold the arrival up
 }
 
+// Columns [col, col + 16 batches) of one row of out, from TMEM: O1 + w1 O2.
+template <int DC>
+__device__ __forceinline__ void store_out(const ScanPass& p, int heads, int head, int64_t r0, int L,
+                                          int row, int col, int batches, float w1,
+                                          uint32_t lane_base, uint32_t powers) {
+  const bool odd = (row & 1) != 0;
+  const uint64_t w2 = f2_pack(w1, w1);
+  const int64_t stride = static_cast<int64_t>(heads) * DC;
+  uint16_t* o = static_cast<uint16_t*>(p.out) + (r0 + (row & ~1)) * stride + head * DC + col + (odd ? 8 : 0);
+  const bool even_row = (row & ~1) < L, odd_row = (row | 1) < L;
+#pragma unroll 1
+  for (int b = 0; b < batches; ++b, col += 16, o += 16) {
+    uint32_t x[16], y[16], z[8];
+    tmem_ld16(lane_base + kColO1 + col, x);
+    tmem_ld16(lane_base + kColO2 + col, y);
+    tmem_wait_ld();
+    tmem_pin16(x);
+    tmem_pin16(y);
+    uint64_t finite = 0ull;  // NaN if some O1 is not finite
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t x2 = f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+      const uint64_t y2 = f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+      finite = f2_fma(x2, 0ull, finite);
+      float u, v;
+      f2_unpack(f2_fma(w2, y2, x2), u, v);
+      z[e] = pack_bf16x2(u, v);
+    }
+    float f0, f1;
+    f2_unpack(finite, f0, f1);
+    // A thread holds 32 bytes of its row; two threads exchange halves so that
+    // their stores cover 32 bytes of one row together.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? z[i] : z[i + 4], 1);
+      if (odd) z[i] = got; else z[i + 4] = got;
+    }
+    if (even_row) *reinterpret_cast<uint4*>(o) = make_uint4(z[0], z[1], z[2], z[3]);
+    if (odd_row) *reinterpret_cast<uint4*>(o + stride) = make_uint4(z[4], z[5], z[6], z[7]);
+    if (__any_sync(0xFFFFFFFFu, f0 != 0.f || f1 != 0.f)) {
+      uint16_t* own_row = static_cast<uint16_t*>(p.out) + (r0 + row) * stride + head * DC + col;
+#pragma unroll 1
+      for (int e = 0; e < 16; ++e) {
+        uint32_t own, share;
+        tmem_ld1(lane_base + kColO1 + col + e, own);
+        tmem_ld1(lane_base + kColO2 + col + e, share);
+        tmem_wait_ld();
+        tmem_pin1(own);
+        tmem_pin1(share);
+        if (row < L && !isfinite(__uint_as_float(own)) && isfinite(__uint_as_float(share)))
+          own_row[e] = static_cast<uint16_t>(
+              pack_bf16x2(fmaf(w1, __uint_as_float(share),
+                               p.out_mul * masked_sum(p, head, r0, L, row, col + e, powers)),
+                          0.f));
+        __syncwarp();
+      }
+    }
+  }
+}
+
 template <int DA, int DC, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1)
     scan_tc_kernel(const __grid_constant__ ScanMaps maps, const __grid_constant__ ScanArgs t) {
@@ -159,9 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* b_ready = bars + 16;           // w b stored
   uint64_t* o_full = bars + 17;            // M3 done (and M2)
   uint64_t* d_full = bars + 18;            // M4 done
-  uint64_t* tab_ready = bars + 19;         // [2] a table of powers stored (state, weight warps)
-  uint64_t* drain = bars + 21;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
+  uint64_t* o_read = bars + 19;            // warps 12-15 have read O1, O2
+  uint64_t* tab_ready = bars + 20;         // [2] a table of powers stored (state, weight warps)
+  uint64_t* drain = bars + 22;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -179,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(b_ready, 8);
     mbar_init(o_full, 1);
     mbar_init(d_full, 1);
+    mbar_init(o_read, 4);
     mbar_init(tab_ready, 8);
     mbar_init(tab_ready + 1, 4);
     mbar_init(drain, 1);
@@ -270,8 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     bool ok = true;
     constexpr uint32_t id_p = idesc_bf16_f32(128, 128, 0, 0);
-    constexpr uint32_t id_o = idesc_bf16_f32(128, DC, 0, 1);
-    constexpr uint32_t id_d = idesc_bf16_f32(128, DC, 1, 1);
+    constexpr uint32_t id_o2 = idesc_bf16_f32(128, DC, 0, 0);
+    constexpr uint32_t id_o1 = idesc_bf16_f32(128, DC, 0, 1);
+    constexpr uint32_t id_64 = idesc_bf16_f32(128, 64, 1, 1);
+    constexpr uint32_t id_128 = idesc_bf16_f32(128, 128, 1, 1);
+    constexpr uint32_t id_192 = idesc_bf16_f32(128, 192, 1, 1);
     uint32_t n = 0;
     // Every lane waits for the issuing one: lanes that ran ahead would poll
     // the next barrier in turns with its instructions.  Products are issued
@@ -299,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t c = 0; c < chunks && ok; ++c, ++n) {
         const uint32_t st = n % kStages, ph = n & 1u;
         const uint32_t d = sbase + st * Pl::kStage;
-        const uint64_t cm = smem_desc(d + Pl::kC, kBox, 1024, 2);  // c, MN-major B
+        const uint64_t cm = smem_desc(d + Pl::kC, kBox, 1024, 2);  // c, MN-major
         bool next = false;
         if (!STATE) {
           if (!ahead) {
@@ -308,14 +372,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) m1(n);
             __syncwarp();
           }
-          if (!warp_wait(s_ready, ph, abort_flag, sticky)) { ok = false; break; }
+          if (!warp_wait(s_ready, ph, abort_flag, sticky) ||
+              (n > 0 && !warp_wait(o_read, (n - 1) & 1u, abort_flag, sticky))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           if (lane == 0) {
             const uint64_t da = smem_desc(d + Pl::kA, 16, 1024, 2);
-            const uint64_t sm = smem_desc(sbase + Pl::kS, Pl::kSBox, 1024, 2);
+            const uint64_t sm = smem_desc(sbase + Pl::kS, 16, 1024, 2);
 #pragma unroll
             for (int g = 0; g < DA / 64; ++g)
-              group(tmem + kColO2, da + g * (kBox >> 4), kStepK, sm + g * 4 * kStepMn, kStepMn, id_o, g == 0);
+              group(tmem + kColO2, da + g * (kBox >> 4), kStepK, sm + g * (Pl::kSBox >> 4), kStepK, id_o2, g == 0);
             mma_commit(a_free);
           }
           __syncwarp();
@@ -326,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int g = 0; g < 2; ++g) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                mma_bf16_ts(tmem + kColO1, tmem + kColP + (g * 4 + i) * 8, cm + (g * 4 + i) * kStepMn, id_o,
+                mma_bf16_ts(tmem + kColO1, tmem + kColP + (g * 4 + i) * 8, cm + (g * 4 + i) * kStepMn, id_o1,
                             g + i > 0 ? 1u : 0u);
             }
             mma_commit(o_full);
@@ -346,20 +414,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(b_ready, ph, abort_flag, sticky)) { ok = false; break; }
         tc_fence_after();
         if (lane == 0) {
-          // w b, MN-major A
+          // c^T times the parts of w b, both MN-major.
+          const bool three = t.p[it.pass].parts == 3;
           const uint64_t hi = smem_desc(d + Pl::kB, kBox, 1024, 2);
-          const uint64_t lo = smem_desc(sbase + Pl::part2(st), kBox, 1024, 2);
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            group(tmem + kColD, hi + g * 4 * kStepMn, kStepMn, cm + g * 4 * kStepMn, kStepMn, id_d, g == 0);
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            group(tmem + kColD, lo + g * 4 * kStepMn, kStepMn, cm + g * 4 * kStepMn, kStepMn, id_d, false);
-          if (t.p[it.pass].parts == 3) {
-            const uint64_t low = smem_desc(sbase + Pl::part3(st), kBox, 1024, 2);
+          auto product = [&](uint64_t part, uint32_t id, bool first) {
 #pragma unroll
             for (int g = 0; g < 2; ++g)
-              group(tmem + kColD, low + g * 4 * kStepMn, kStepMn, cm + g * 4 * kStepMn, kStepMn, id_d, false);
+              group(tmem + Pl::kColD, cm + g * 4 * kStepMn, kStepMn, part + g * 4 * kStepMn, kStepMn, id,
+                    first && g == 0);
+          };
+          if (Pl::kOwn) {
+            // One product for the parts side by side, 64 columns of D each;
+            // with dc = 128 TMEM has room for two of them.
+            product(hi, DC == 64 && three ? id_192 : id_128, true);
+            if (DC == 128 && three) product(smem_desc(d + Pl::kB + 2 * kBox, kBox, 1024, 2), id_64, false);
+          } else {
+            product(hi, id_128, true);
+            product(smem_desc(d + Pl::kA, kBox, 1024, 2), id_128, false);
+            if (three) product(smem_desc(sbase + Pl::kS, kBox, 1024, 2), id_128, false);
           }
           mma_commit(empty + st);
           mma_commit(d_full);
@@ -376,16 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ state
     bool ok = true;
     const int q = warp & 3, hf = (warp - 4) >> 2, ctid = tid - 128;
-    const int row = q * 32 + lane;  // TMEM lane: row of the state
+    const int row = q * 32 + lane;  // TMEM lane: column of the state (row of S^T), row of out
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t tab = 0, items = 0, n = 0;
-    constexpr int HC = DC / 2;
-    const bool state_row = DA == 128 || q < 2;
-    uint64_t S[HC / 2];  // pairs of columns
+    constexpr int HA = DA / 2;
+    const bool state_row = DC == 128 || q < 2;
+    uint64_t S[HA / 2];  // pairs of rows of the state
     ScanItem it;
     auto power = [&](int e) { return ld_shared_f32(tab + e * 4); };
     // S <- (f + fl) S + D, once M4 of the chunk before is done.
-    auto add_d = [&](float f, float fl) {
+    auto add_d = [&](float f, float fl, bool three) {
       if (!ok || !warp_wait(d_full, (n - 1) & 1u, abort_flag, sticky)) {
         ok = false;
         return;
@@ -394,11 +466,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (state_row) {
         const uint64_t f2 = f2_pack(f, f), fl2 = f2_pack(fl, fl);
 #pragma unroll
-        for (int j = 0; j < HC / 16; ++j) {
-          uint32_t v[16];
-          tmem_ld16(lane_base + kColD + hf * HC + j * 16, v);
+        for (int j = 0; j < HA / 16; ++j) {
+          uint32_t v[16], lo[16];
+          tmem_ld16(lane_base + Pl::kColD + hf * HA + j * 16, v);
+          if (Pl::kOwn) tmem_ld16(lane_base + Pl::kColD + 64 + hf * HA + j * 16, lo);
           tmem_wait_ld();
           tmem_pin16(v);
+          if (Pl::kOwn) {
+            tmem_pin16(lo);
+            if (DC == 64 && three) {
+              uint32_t low[16];
+              tmem_ld16(lane_base + Pl::kColD + 128 + hf * HA + j * 16, low);
+              tmem_wait_ld();
+              tmem_pin16(low);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                lo[e] = __float_as_uint(__uint_as_float(lo[e]) + __uint_as_float(low[e]));
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(lo[e]));
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             S[j * 8 + e] = f2_fma(f2, S[j * 8 + e],
@@ -424,10 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* src = STATE ? nullptr : seg ? p.bound : p.ends;
         const float m = seg ? 1.f : p.ends_mul;
         const int64_t o = (seg ? it.from : it.state) * (DA * DC);
-        const int step = p.transposed ? DA : 1;
-        const int64_t first = o + (p.transposed ? row + hf * HC * DA : row * DC + hf * HC);
+        const int step = p.transposed ? 1 : DC;
+        const int64_t first = o + (p.transposed ? row * DA + hf * HA : hf * HA * DC + row);
 #pragma unroll
-        for (int j = 0; j < HC / 2; ++j)
+        for (int j = 0; j < HA / 2; ++j)
           S[j] = src == nullptr ? 0ull
                                 : f2_pack(m * src[first + (2 * j) * step], m * src[first + (2 * j + 1) * step]);
       }
@@ -446,32 +534,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int skip = rev && it.first && c == 0 ? 1 : 0;
         // s3: w b in two or three bf16 parts, the first one over b.
         auto split = [&]() {
+          constexpr int kRowStep = kStateThreads / (DA / 8);  // a multiple of 8
+          const int u = ctid % (DA / 8), first = ctid / (DA / 8);
+          const uint32_t o = (u >> 3) * kBox + swz(first, u & 7);
+          uint32_t src = d + Pl::kB + o;
+          uint32_t dst = Pl::kOwn ? src + kBox : d + Pl::kA + o;
+          uint32_t third = Pl::kOwn ? src + 2 * kBox : sbase + Pl::kS + o;
+          const bool three = p.parts == 3;
+          const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll 2
-          for (int e = ctid; e < 128 * (DA / 8); e += kStateThreads) {
-            const int r = e / (DA / 8), u = e % (DA / 8);
-            const uint32_t o = (u >> 3) * kBox + swz(r, u & 7), src = d + Pl::kB + o;
+          for (int r = first; r < 128; r += kRowStep) {
             const float w1 = r < L ? power(rev ? r : L - 1 - r) : 0.f;
-            const uint64_t w = f2_pack(w1, w1), minus = f2_pack(-1.f, -1.f);
+            const uint64_t w = f2_pack(w1, w1);
             const uint4 x = ld_shared_v4u(src);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-            uint32_t hi[4], lo[4], low[4];
+            uint32_t v[4] = {x.x, x.y, x.z, x.w};
+            if (r >= L) v[0] = v[1] = v[2] = v[3] = 0u;
+            uint64_t y[4];
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t v = r < L ? xs[i] : 0u;
-              uint64_t y = f2_mul(w, f2_pack(bf_lo(v), bf_hi(v)));
+              y[i] = f2_mul(w, f2_pack(bf_lo(v[i]), bf_hi(v[i])));
               float y0, y1;
-              f2_unpack(y, y0, y1);
+              f2_unpack(y[i], y0, y1);
               hi[i] = pack_bf16x2(y0, y1);
-              y = f2_fma(minus, f2_pack(bf_lo(hi[i]), bf_hi(hi[i])), y);
-              f2_unpack(y, y0, y1);
+              y[i] = f2_fma(minus, f2_pack(bf_lo(hi[i]), bf_hi(hi[i])), y[i]);
+              f2_unpack(y[i], y0, y1);
               lo[i] = pack_bf16x2(y0, y1);
-              y = f2_fma(minus, f2_pack(bf_lo(lo[i]), bf_hi(lo[i])), y);
-              f2_unpack(y, y0, y1);
-              low[i] = pack_bf16x2(y0, y1);
             }
             st_shared_v4(src, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(sbase + Pl::part2(st) + o, lo[0], lo[1], lo[2], lo[3]);
-            if (p.parts == 3) st_shared_v4(sbase + Pl::part3(st) + o, low[0], low[1], low[2], low[3]);
+            st_shared_v4(dst, lo[0], lo[1], lo[2], lo[3]);
+            if (three) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float y0, y1;
+                f2_unpack(f2_fma(minus, f2_pack(bf_lo(lo[i]), bf_hi(lo[i])), y[i]), y0, y1);
+                hi[i] = pack_bf16x2(y0, y1);
+              }
+              st_shared_v4(third, hi[0], hi[1], hi[2], hi[3]);
+            }
+            src += kRowStep * 128, dst += kRowStep * 128, third += kRowStep * 128;
           }
         };
         if (!warp_wait(full + st, (n / kStages) & 1u, abort_flag, sticky)) { ok = false; break; }
@@ -488,15 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           split();
         }
         // s1
-        if (c > 0) add_d(f, fl);
+        if (c > 0) add_d(f, fl, p.parts == 3);
         if (!ok) break;
         f = power(L - skip);
         fl = L - skip == 128 ? power(129) : 0.f;
         if (!STATE) {
           if (state_row) {
 #pragma unroll
-            for (int u = 0; u < HC / 8; ++u) {
-              const int col = hf * HC + u * 8;
+            for (int u = 0; u < HA / 8; ++u) {
+              const int col = hf * HA + u * 8;
               uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -523,66 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
           tc_fence_after();
           const float w1 = p.out_mul * power(row < L ? (rev ? L - row : row + 1) - skip : 0);
-          const uint64_t w2 = f2_pack(w1, w1), mul = f2_pack(p.out_mul, p.out_mul);
-#pragma unroll 1
-          for (int col = hf * HC; col < hf * HC + HC; col += 16) {
-            uint32_t x1[16], y[16], z[8];
-            tmem_ld16(lane_base + kColO1 + col, x1);
-            tmem_ld16(lane_base + kColO2 + col, y);
-            tmem_wait_ld();
-            tmem_pin16(x1);
-            tmem_pin16(y);
-            uint64_t finite = 0ull;  // NaN if some O1 is not finite
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint64_t x2 = f2_pack(__uint_as_float(x1[2 * e]), __uint_as_float(x1[2 * e + 1]));
-              const uint64_t y2 = f2_pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
-              finite = f2_fma(x2, 0ull, finite);
-              float u, v;
-              f2_unpack(f2_fma(w2, y2, f2_mul(mul, x2)), u, v);
-              z[e] = pack_bf16x2(u, v);
-            }
-            float f0, f1;
-            f2_unpack(finite, f0, f1);
-            // A thread holds 32 bytes of its row; two threads exchange halves
-            // so that their stores cover 32 bytes of one row together.
-            const bool odd = (lane & 1) != 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? z[i] : z[i + 4], 1);
-              if (odd) z[i] = got; else z[i + 4] = got;
-            }
-            uint16_t* o = static_cast<uint16_t*>(p.out) +
-                          ((r0 + (row & ~1)) * t.s.heads + it.head) * DC + col + (odd ? 8 : 0);
-            if ((row & ~1) < L) *reinterpret_cast<uint4*>(o) = make_uint4(z[0], z[1], z[2], z[3]);
-            if ((row | 1) < L)
-              *reinterpret_cast<uint4*>(o + static_cast<int64_t>(t.s.heads) * DC) =
-                  make_uint4(z[4], z[5], z[6], z[7]);
-            if (__any_sync(0xFFFFFFFFu, f0 != 0.f || f1 != 0.f)) {
-              uint16_t* own_row = static_cast<uint16_t*>(p.out) +
-                                  ((r0 + row) * t.s.heads + it.head) * DC + col;
-#pragma unroll 1
-              for (int e = 0; e < 16; ++e) {
-                uint32_t own, share;
-                tmem_ld1(lane_base + kColO1 + col + e, own);
-                tmem_ld1(lane_base + kColO2 + col + e, share);
-                tmem_wait_ld();
-                tmem_pin1(own);
-                tmem_pin1(share);
-                if (row < L && !isfinite(__uint_as_float(own)) && isfinite(__uint_as_float(share)))
-                  own_row[e] = static_cast<uint16_t>(
-                      pack_bf16x2(fmaf(w1, __uint_as_float(share),
-                                       p.out_mul * masked_sum(p, it.head, r0, L, row, col + e, tab)),
-                                  0.f));
-                __syncwarp();
-              }
-            }
-          }
+          constexpr int kCols = (DC - kSideCols) / 2;
+          store_out<DC>(p, t.s.heads, it.head, r0, L, row, hf * kCols, kCols / 16, w1, lane_base, tab);
           tc_fence_before();
         }
       }
       if (!ok) break;
-      if (chunks > 0) add_d(f, fl);
+      if (chunks > 0) add_d(f, fl, p.parts == 3);
       if (!ok) break;
       // The state behind the last row.
       float* dst = nullptr;
@@ -598,12 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (dst != nullptr && state_row) {
 #pragma unroll
-        for (int j = 0; j < HC / 4; ++j) {
-          float4 v;
-          f2_unpack(S[2 * j], v.x, v.y);
-          f2_unpack(S[2 * j + 1], v.z, v.w);
-          v.x *= m, v.y *= m, v.z *= m, v.w *= m;
-          *reinterpret_cast<float4*>(dst + o + row * DC + hf * HC + j * 4) = v;
+        for (int j = 0; j < HA / 2; ++j) {
+          float x, y;
+          f2_unpack(S[j], x, y);
+          dst[o + (hf * HA + 2 * j) * DC + row] = m * x;
+          dst[o + (hf * HA + 2 * j + 1) * DC + row] = m * y;
         }
       }
     }
@@ -631,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ph = n & 1u;
         const int64_t r0 = it.lo + 128 * (rev ? chunks - 1 - c : c);
         const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
+        const int skip = rev && it.first && c == 0 ? 1 : 0;
         // s2: 32 columns of P at a time; their 16 columns of P~ go where
         // columns lay that have been read.  A block of 32 x 32 that the scan
         // covers whole has the weight E F_j, both powers with exponents >= 0;
@@ -652,14 +700,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const int dist = rev ? e - lane : lane - e;
-                const float w = power(dist >= 0 ? dist : 0);
+                const float w = p.out_mul * power(dist >= 0 ? dist : 0);
                 v[e] = dist >= 0 ? __float_as_uint(__uint_as_float(v[e]) * w) : 0u;
               }
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 o[e] = pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
             } else {
-              const float E1 = power(rev ? jb * 32 - row : row - jb * 32 - 31);
+              const float E1 = p.out_mul * power(rev ? jb * 32 - row : row - jb * 32 - 31);
               const uint64_t E = f2_pack(E1, E1);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -683,6 +731,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(p_ready, lane);
+        // s4
+        if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
+        tc_fence_after();
+        const float w1 = p.out_mul * power(row < L ? (rev ? L - row : row + 1) - skip : 0);
+        store_out<DC>(p, t.s.heads, it.head, r0, L, row, DC - kSideCols, kSideCols / 16, w1, lane_base, tab);
+        tc_fence_before();
+        warp_arrive(o_read, lane);
       }
       if (!ok) break;
     }
