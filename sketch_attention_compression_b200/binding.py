@@ -8,6 +8,7 @@ fallback: if libsa.so is missing or a call fails, an exception is raised.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -155,9 +156,15 @@ def _check(status: int, what: str) -> None:
         raise SAError(status, what)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch  # deferred: the binding is importable without torch for the ABI checks
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch  # deferred: the binding is importable without torch for the ABI checks
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream) -> int:
@@ -730,55 +737,73 @@ class ActionFusion:
 
 
 # ---------------------------------------------------------------- linear attention
+#
+# The smallest calls of the operators below take a few microseconds on the
+# GPU, so their checks look at each property of a tensor once and build a
+# message only to raise it.
 
 
-def _strided(t, name, heads_shape, dtype):
-    """(pointer, row stride, head stride) of a (rows, heads, d) CUDA tensor
+def _current_device(torch):
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _stream_of(stream, device):
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(device)
+    return _stream_handle(stream)
+
+
+def _on_device(t, name, device):
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _strided(t, name, shape, dtype, device):
+    """(address, row stride, head stride) of a (rows, heads, d) CUDA tensor
     whose last dimension is adjacent in memory."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.get_device() != device:
+        _on_device(t, name, device)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, like q")
-    if tuple(t.shape) != heads_shape:
-        raise ValueError(f"{name} must have shape {heads_shape}")
-    if t.stride(2) != 1 and t.numel() > 0:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}")
+    row, head, last = t.stride()
+    if last != 1 and t.numel() > 0:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr() if t.numel() > 0 else None, t.stride(0), t.stride(1)
+    return t.data_ptr(), row, head
 
 
-def _optional(t, name, shape, dtype):
-    """Pointer of a dense CUDA tensor of that shape and type; None for None."""
+def _vector(t, name, shape, dtype, device):
+    """Address of a dense CUDA tensor of that shape and type; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {shape}")
-    if t.numel() == 0:
-        return None
-    return _dev_ptr(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        _on_device(t, name, device)
+    return t.data_ptr()
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: every operand must live there."""
-    current = _torch().cuda.current_device() if any(
-        t is not None and t.is_cuda for t in tensors) else -1
-    for t in tensors:
-        if t is not None and t.get_device() != current:
-            raise ValueError("every tensor must be on the current CUDA device")
+def _buffer(t, name, device):
+    """(address, bytes) of a dense CUDA tensor; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        _on_device(t, name, device)
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _attention_shapes(q, v):
+def _attention_shapes(q, v, offsets):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be (rows, heads, d)")
-    rows, heads, d_k = (int(x) for x in q.shape)
-    return rows, heads, d_k, int(v.shape[2])
-
-
-def _attention_workspace(lib, workspace, device, *sizes):
-    if workspace is None:
-        workspace = _torch().empty(lib.sa_workspace_bytes_linear_attention(*sizes) or 256,
-                                   dtype=_torch().uint8, device=device)
-    return workspace, _dev_ptr(workspace, "workspace"), \
-        int(workspace.numel() * workspace.element_size())
+    if offsets is not None and (offsets.dtype is not _torch().int64 or offsets.dim() != 1):
+        raise TypeError("offsets must be a 1-D int64 tensor")
+    rows, heads, d_k = q.shape
+    return rows, heads, d_k, v.shape[2], 0 if offsets is None else offsets.shape[0] - 1
 
 
 def linear_attention_forward(q, k, v, log_decay, offsets, scale, initial_state=None,
@@ -794,29 +819,28 @@ def linear_attention_forward(q, k, v, log_decay, offsets, scale, initial_state=N
     d_v) fp32 or None; max_rows a bound on the longest history, if known.
     Returns (out (N, H, d_v), final_state (B, H, d_k, d_v) fp32, workspace);
     final_state may be given as initial_state itself."""
-    torch = _torch()
-    lib = load_library()
-    N, H, dk, dv = _attention_shapes(q, v)
-    if offsets.dtype != torch.int64 or offsets.dim() != 1:
-        raise TypeError("offsets must be a 1-D int64 tensor")
-    B = int(offsets.shape[0]) - 1
+    torch, lib = _torch(), load_library()
+    dtype, f32, device = q.dtype, torch.float32, _current_device(torch)
+    N, H, dk, dv, B = _attention_shapes(q, v, offsets)
     states = (B, H, dk, dv)
-    args = (*_strided(q, "q", (N, H, dk), q.dtype), *_strided(k, "k", (N, H, dk), q.dtype),
-            *_strided(v, "v", (N, H, dv), q.dtype))
-    if out is None:
-        out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
-    if final_state is None:
-        final_state = torch.empty(states, dtype=torch.float32, device=q.device)
+    args = (*_strided(q, "q", (N, H, dk), dtype, device), *_strided(k, "k", (N, H, dk), dtype, device),
+            *_strided(v, "v", (N, H, dv), dtype, device))
     bound = 0 if max_rows is None else int(max_rows)
-    workspace, wp, wn = _attention_workspace(lib, workspace, q.device, H, dk, dv, B, N, bound)
-    _on_current_device(q, k, v, log_decay, offsets, initial_state, out, final_state, workspace)
+    if out is None:
+        out = torch.empty((N, H, dv), dtype=dtype, device=q.device)
+    if final_state is None:
+        final_state = torch.empty(states, dtype=f32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
+                                dtype=torch.uint8, device=q.device)
     _check(lib.sa_linear_attention_forward(
-        *args, _optional(log_decay, "log_decay", (H,), torch.float32), _dev_ptr(offsets, "offsets"),
-        B, N, bound, H, dk, dv, _dtype_code(q.dtype), float(scale),
-        _optional(initial_state, "initial_state", states, torch.float32),
-        _optional(out, "out", (N, H, dv), q.dtype),
-        _optional(final_state, "final_state", states, torch.float32), wp, wn,
-        _stream_handle(stream)), "sa_linear_attention_forward")
+        *args, _vector(log_decay, "log_decay", (H,), f32, device), _buffer(offsets, "offsets", device)[0],
+        B, N, bound, H, dk, dv, _dtype_code(dtype), float(scale),
+        _vector(initial_state, "initial_state", states, f32, device),
+        _vector(out, "out", (N, H, dv), dtype, device),
+        _vector(final_state, "final_state", states, f32, device),
+        *_buffer(workspace, "workspace", device), _stream_of(stream, device)),
+        "sa_linear_attention_forward")
     return out, final_state, workspace
 
 
@@ -826,32 +850,31 @@ def linear_attention_backward(q, k, v, log_decay, offsets, scale, d_out, initial
     for d_out = dL/d out (N, H, d_v) and d_final_state = dL/d final_state or
     None.  Returns dict(dq, dk, dv, and d_initial_state where an initial
     state is given) and the workspace."""
-    torch = _torch()
-    lib = load_library()
-    N, H, dk, dv = _attention_shapes(q, v)
-    if offsets.dtype != torch.int64 or offsets.dim() != 1:
-        raise TypeError("offsets must be a 1-D int64 tensor")
-    B = int(offsets.shape[0]) - 1
+    torch, lib = _torch(), load_library()
+    dtype, f32, device = q.dtype, torch.float32, _current_device(torch)
+    N, H, dk, dv, B = _attention_shapes(q, v, offsets)
     states = (B, H, dk, dv)
-    args = (*_strided(q, "q", (N, H, dk), q.dtype), *_strided(k, "k", (N, H, dk), q.dtype),
-            *_strided(v, "v", (N, H, dv), q.dtype))
-    grad = _strided(d_out, "d_out", (N, H, dv), q.dtype)
-    out = dict(dq=torch.empty((N, H, dk), dtype=q.dtype, device=q.device),
-               dk=torch.empty((N, H, dk), dtype=q.dtype, device=q.device),
-               dv=torch.empty((N, H, dv), dtype=q.dtype, device=q.device))
-    if initial_state is not None:
-        out["d_initial_state"] = torch.empty(states, dtype=torch.float32, device=q.device)
+    args = (*_strided(q, "q", (N, H, dk), dtype, device), *_strided(k, "k", (N, H, dk), dtype, device),
+            *_strided(v, "v", (N, H, dv), dtype, device))
+    grad = _strided(d_out, "d_out", (N, H, dv), dtype, device)
     bound = 0 if max_rows is None else int(max_rows)
-    workspace, wp, wn = _attention_workspace(lib, workspace, q.device, H, dk, dv, B, N, bound)
-    _on_current_device(q, k, v, log_decay, offsets, d_out, initial_state, d_final_state, workspace)
+    out = dict(dq=torch.empty((N, H, dk), dtype=dtype, device=q.device),
+               dk=torch.empty((N, H, dk), dtype=dtype, device=q.device),
+               dv=torch.empty((N, H, dv), dtype=dtype, device=q.device))
+    ds0 = None
+    if initial_state is not None:
+        ds0 = out["d_initial_state"] = torch.empty(states, dtype=f32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
+                                dtype=torch.uint8, device=q.device)
     _check(lib.sa_linear_attention_backward(
-        *args, _optional(log_decay, "log_decay", (H,), torch.float32), _dev_ptr(offsets, "offsets"),
-        B, N, bound, H, dk, dv, _dtype_code(q.dtype), float(scale),
-        _optional(initial_state, "initial_state", states, torch.float32), *grad,
-        _optional(d_final_state, "d_final_state", states, torch.float32),
-        *(out[x].data_ptr() if N > 0 else None for x in ("dq", "dk", "dv")),
-        out["d_initial_state"].data_ptr() if initial_state is not None else None, wp, wn,
-        _stream_handle(stream)), "sa_linear_attention_backward")
+        *args, _vector(log_decay, "log_decay", (H,), f32, device), _buffer(offsets, "offsets", device)[0],
+        B, N, bound, H, dk, dv, _dtype_code(dtype), float(scale),
+        _vector(initial_state, "initial_state", states, f32, device), *grad,
+        _vector(d_final_state, "d_final_state", states, f32, device),
+        out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(),
+        None if ds0 is None else ds0.data_ptr(), *_buffer(workspace, "workspace", device),
+        _stream_of(stream, device)), "sa_linear_attention_backward")
     return out, workspace
 
 
@@ -862,53 +885,51 @@ def linear_attention_step(state, q, k, v, log_decay, scale, slots=None, out=None
     v (B, H, d_v) bf16 or fp32; slots (B,) int64: the state of each entry (a
     negative slot marks a padded entry), or None for entry b's state b.
     Returns out (B, H, d_v)."""
-    torch = _torch()
-    lib = load_library()
-    B, H, dk, dv = _attention_shapes(q, v)
+    torch, lib = _torch(), load_library()
+    dtype, f32, device = q.dtype, torch.float32, _current_device(torch)
+    B, H, dk, dv, _ = _attention_shapes(q, v, None)
     if state.dim() != 4:
         raise ValueError("state must be (states, heads, d_k, d_v)")
+    S = state.shape[0]
+    args = (*_strided(q, "q", (B, H, dk), dtype, device), *_strided(k, "k", (B, H, dk), dtype, device),
+            *_strided(v, "v", (B, H, dv), dtype, device))
     if out is None:
-        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
-    S = int(state.shape[0])
-    _on_current_device(state, q, k, v, log_decay, slots, out, device_flags)
+        out = torch.empty((B, H, dv), dtype=dtype, device=q.device)
     _check(lib.sa_linear_attention_step(
-        *_strided(q, "q", (B, H, dk), q.dtype), *_strided(k, "k", (B, H, dk), q.dtype),
-        *_strided(v, "v", (B, H, dv), q.dtype),
-        _optional(log_decay, "log_decay", (H,), torch.float32),
-        _optional(slots, "slots", (B,), torch.int64), B, S, H, dk, dv, _dtype_code(q.dtype),
-        float(scale), _optional(state, "state", (S, H, dk, dv), torch.float32),
-        _optional(out, "out", (B, H, dv), q.dtype),
-        None if device_flags is None else _dev_ptr(device_flags, "device_flags"),
-        _stream_handle(stream)), "sa_linear_attention_step")
+        *args, _vector(log_decay, "log_decay", (H,), f32, device),
+        _vector(slots, "slots", (B,), torch.int64, device), B, S, H, dk, dv, _dtype_code(dtype), float(scale),
+        _vector(state, "state", (S, H, dk, dv), f32, device),
+        _vector(out, "out", (B, H, dv), dtype, device),
+        _buffer(device_flags, "device_flags", device)[0], _stream_of(stream, device)),
+        "sa_linear_attention_step")
     return out
 
 
 # ---------------------------------------------------------------- norms around a block
 
 
-def _rows2d(t, name, shape, dtype):
-    """(pointer, row stride) of a tensor of (..., d) rows at one stride."""
+def _rows(t, name, shape, dtype, device):
+    """(address, row stride) of a tensor of (..., d) rows at one stride.  An
+    empty tensor has an address too: the library takes NULL for an operand
+    that is left out."""
     if t is None:
         return None, 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {shape}")
-    if t.numel() == 0:
-        return t.data_ptr() or 256, shape[-1]
+    if t.get_device() != device:
+        _on_device(t, name, device)
     if t.is_contiguous():
-        return t.data_ptr(), shape[-1]
+        return t.data_ptr() or 256, shape[-1]
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows")
     return t.data_ptr(), t.stride(0)
 
 
-def _norm_params(d, kind, gate_kind, **vectors):
+def _norm_kinds(kind, gate_kind):
     if kind not in SA_NORM_KINDS or gate_kind not in SA_GATE_KINDS:
         raise ValueError(f"kind must be one of {sorted(SA_NORM_KINDS)}, gate_kind one of "
                          f"{sorted(SA_GATE_KINDS)}")
-    f32 = _torch().float32
-    return [_optional(t, name, (d,), f32) for name, t in vectors.items()]
+    return SA_NORM_KINDS[kind], SA_GATE_KINDS[gate_kind]
 
 
 def block_norm_forward(residual, block=None, gate=None, post_gain=None, post_bias=None,
@@ -925,40 +946,37 @@ def block_norm_forward(residual, block=None, gate=None, post_gain=None, post_bia
     fp32 residual takes either); the parameters (d,) fp32.  What is None is
     left out; without a block only u is computed, in `dtype` (the residual's
     by default).  Returns (r, u), None for what is not computed."""
-    torch = _torch()
-    lib = load_library()
-    shape = tuple(residual.shape)
-    d = int(shape[-1])
+    torch, lib = _torch(), load_library()
+    shape, tr, f32, device = residual.shape, residual.dtype, torch.float32, _current_device(torch)
+    d = shape[-1]
     rows = residual.numel() // d if d > 0 else 0
     if block is not None:
         dtype = block.dtype
     elif dtype is None:
-        dtype = residual.dtype
-    params = _norm_params(d, kind, gate_kind, post_gain=post_gain, post_bias=post_bias,
-                          res_scale=res_scale, pre_gain=pre_gain, pre_bias=pre_bias)
+        dtype = tr
+    kinds = _norm_kinds(kind, gate_kind)
+    x = _rows(residual, "residual", shape, tr, device)
     if block is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=residual.dtype, device=residual.device)
+        residual_out = torch.empty(shape, dtype=tr, device=residual.device)
     if pre_gain is not None and normed is None:
         normed = torch.empty(shape, dtype=dtype, device=residual.device)
-    _on_current_device(residual, block, gate, post_gain, post_bias, res_scale, pre_gain, pre_bias,
-                       residual_out, normed)
+    v = (d,)
     _check(lib.sa_block_norm_forward(
-        *_rows2d(residual, "residual", shape, residual.dtype), *_rows2d(block, "block", shape, dtype),
-        *_rows2d(gate, "gate", shape, dtype), *params, rows, d, _dtype_code(residual.dtype),
-        _dtype_code(dtype), SA_NORM_KINDS[kind], SA_GATE_KINDS[gate_kind], float(eps),
-        _dense(residual_out, "residual_out", shape, residual.dtype),
-        _dense(normed, "normed", shape, dtype), _stream_handle(stream)), "sa_block_norm_forward")
+        *x, *_rows(block, "block", shape, dtype, device), *_rows(gate, "gate", shape, dtype, device),
+        _vector(post_gain, "post_gain", v, f32, device), _vector(post_bias, "post_bias", v, f32, device),
+        _vector(res_scale, "res_scale", v, f32, device), _vector(pre_gain, "pre_gain", v, f32, device),
+        _vector(pre_bias, "pre_bias", v, f32, device), rows, d, _dtype_code(tr), _dtype_code(dtype),
+        *kinds, float(eps), _dense(residual_out, "residual_out", shape, tr, device),
+        _dense(normed, "normed", shape, dtype, device), _stream_of(stream, device)),
+        "sa_block_norm_forward")
     return residual_out, normed
 
 
-def _dense(t, name, shape, dtype):
-    """Pointer of a dense output; not None for an empty one, which the
-    library takes for an output that is asked for."""
+def _dense(t, name, shape, dtype, device):
+    """Address of a dense output, also of an empty one; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {shape}")
-    return _dev_ptr(t, name) if t.numel() > 0 else 256
+    return _vector(t, name, shape, dtype, device) or 256
 
 
 def block_norm_backward(residual_out, block, d_residual_out, d_normed, gate=None, post_gain=None,
@@ -970,95 +988,108 @@ def block_norm_backward(residual_out, block, d_residual_out, d_normed, gate=None
     dL/du (None without a pre_gain).  Returns a dict of d_residual, and of
     d_block, d_gate, d_post_gain, d_post_bias, d_res_scale, d_pre_gain,
     d_pre_bias for the operands given."""
-    torch = _torch()
-    lib = load_library()
-    shape = tuple(residual_out.shape)
-    d = int(shape[-1])
+    torch, lib = _torch(), load_library()
+    shape, tr, f32 = residual_out.shape, residual_out.dtype, torch.float32
+    device, dev = _current_device(torch), residual_out.device
+    d = shape[-1]
     rows = residual_out.numel() // d if d > 0 else 0
-    tr, dev = residual_out.dtype, residual_out.device
     if block is not None:
         dtype = block.dtype
     elif dtype is None:
         dtype = tr if d_normed is None else d_normed.dtype
-    params = _norm_params(d, kind, gate_kind, post_gain=post_gain, post_bias=post_bias,
-                          res_scale=res_scale, pre_gain=pre_gain, pre_bias=pre_bias)
+    kinds = _norm_kinds(kind, gate_kind)
+    v = (d,)
+    r = _rows(residual_out, "residual_out", shape, tr, device)
+    params = [_vector(post_gain, "post_gain", v, f32, device),
+              _vector(post_bias, "post_bias", v, f32, device),
+              _vector(res_scale, "res_scale", v, f32, device),
+              _vector(pre_gain, "pre_gain", v, f32, device),
+              _vector(pre_bias, "pre_bias", v, f32, device)]
     out = dict(d_residual=torch.empty(shape, dtype=tr, device=dev))
-    for name, t in (("d_block", block), ("d_gate", gate)):
-        if t is not None:
-            out[name] = torch.empty(shape, dtype=dtype, device=dev)
+    if block is not None:
+        out["d_block"] = torch.empty(shape, dtype=dtype, device=dev)
+    if gate is not None:
+        out["d_gate"] = torch.empty(shape, dtype=dtype, device=dev)
     sums = []
-    for name, t in (("d_post_gain", post_gain), ("d_post_bias", post_bias),
-                    ("d_res_scale", res_scale), ("d_pre_gain", pre_gain), ("d_pre_bias", pre_bias)):
-        if t is not None:
-            out[name] = torch.empty((d,), dtype=torch.float32, device=dev)
-        sums.append(out[name].data_ptr() if t is not None else None)
+    for name, p in zip(("d_post_gain", "d_post_bias", "d_res_scale", "d_pre_gain", "d_pre_bias"),
+                       params):
+        if p is None:
+            sums.append(None)
+            continue
+        out[name] = torch.empty(v, dtype=f32, device=dev)
+        sums.append(out[name].data_ptr())
     if workspace is None and any(sums):
         workspace = torch.empty(lib.sa_workspace_bytes_block_norm(rows, d) or 16, dtype=torch.uint8,
                                 device=dev)
-    _on_current_device(residual_out, block, gate, d_residual_out, d_normed, post_gain, post_bias,
-                       res_scale, pre_gain, pre_bias, workspace)
     _check(lib.sa_block_norm_backward(
-        *_rows2d(residual_out, "residual_out", shape, tr), *_rows2d(block, "block", shape, dtype),
-        *_rows2d(gate, "gate", shape, dtype), *params[:4], rows, d, _dtype_code(tr),
-        _dtype_code(dtype), SA_NORM_KINDS[kind], SA_GATE_KINDS[gate_kind], float(eps),
-        *_rows2d(d_residual_out, "d_residual_out", shape, tr),
-        *_rows2d(d_normed, "d_normed", shape, dtype),
-        *(_dense(out.get(name), name, shape, t) for name, t in (
-            ("d_residual", tr), ("d_block", dtype), ("d_gate", dtype))), *sums,
-        None if workspace is None else _dev_ptr(workspace, "workspace"),
-        0 if workspace is None else int(workspace.numel() * workspace.element_size()),
-        _stream_handle(stream)), "sa_block_norm_backward")
+        *r, *_rows(block, "block", shape, dtype, device), *_rows(gate, "gate", shape, dtype, device),
+        *params[:4], rows, d, _dtype_code(tr), _dtype_code(dtype), *kinds, float(eps),
+        *_rows(d_residual_out, "d_residual_out", shape, tr, device),
+        *_rows(d_normed, "d_normed", shape, dtype, device),
+        _dense(out["d_residual"], "d_residual", shape, tr, device),
+        _dense(out.get("d_block"), "d_block", shape, dtype, device),
+        _dense(out.get("d_gate"), "d_gate", shape, dtype, device), *sums,
+        *_buffer(workspace, "workspace", device), _stream_of(stream, device)),
+        "sa_block_norm_backward")
     return out
 
 
 # ---------------------------------------------------------------- gradient norm
 
 
-def _tensor_table(tensors, name):
-    """(addresses, sizes, types) of dense CUDA tensors as ctypes arrays."""
-    n = len(tensors)
-    bf16, f32 = _torch().bfloat16, _torch().float32
-    codes = []
-    for t in tensors:
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous CUDA tensors")
-        if t.dtype == bf16:
-            codes.append(SA_BF16)
-        elif t.dtype == f32:
-            codes.append(SA_FP32)
-        else:
-            raise TypeError(f"{name} must be bfloat16 or float32")
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), (ctypes.c_int * n)(*codes))
+def _tensor_table(torch, tensors, name, device):
+    """(addresses, sizes, types) of dense CUDA tensors, as lists."""
+    codes = {torch.bfloat16: SA_BF16, torch.float32: SA_FP32}
+    try:
+        types = [codes[t.dtype] for t in tensors]
+    except KeyError:
+        raise TypeError(f"{name} must be bfloat16 or float32") from None
+    if [t.get_device() for t in tensors].count(device) != len(tensors):
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name} must be contiguous CUDA tensors")
+    return [t.data_ptr() for t in tensors], [t.numel() for t in tensors], types
 
 
-def _norm_buffers(lib, tensors, norm, workspace, device):
-    torch = _torch()
-    if len(tensors) == 0 and device is None:
+def _clip(torch, lib, grads, max_norm, out, norm, workspace, device, stream):
+    """sa_grad_norm (max_norm None) or sa_clip_grad_norm."""
+    grads = list(grads)
+    n = len(grads)
+    if n == 0 and device is None:
         raise ValueError("device is needed when there are no gradients")
-    device = tensors[0].device if len(tensors) > 0 else device
+    current = _current_device(torch) if n > 0 else torch.cuda.current_device()
+    addresses, sizes, types = _tensor_table(torch, grads, "grads", current)
+    targets = None
+    if out is not None:
+        out = list(out)
+        to, to_sizes, to_types = _tensor_table(torch, out, "out", current)
+        if to_types != types or to_sizes != sizes or [t.shape for t in out] != [t.shape for t in grads]:
+            raise ValueError("out must match grads in number, shapes and types")
+        targets = array.array("Q", to)
+    device = grads[0].device if n > 0 else device
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=device)
-    elif norm.dtype != torch.float32 or norm.numel() != 1:
+    elif norm.dtype is not torch.float32 or norm.numel() != 1:
         raise ValueError("norm must hold one float32")
     if workspace is None:
-        workspace = torch.empty(lib.sa_workspace_bytes_grad_norm(len(tensors)), dtype=torch.uint8,
-                                device=device)
-    _on_current_device(norm, workspace, *tensors)
-    return norm, (_dev_ptr(norm, "norm"), _dev_ptr(workspace, "workspace"),
-                  int(workspace.numel() * workspace.element_size()))
+        workspace = torch.empty(lib.sa_workspace_bytes_grad_norm(n), dtype=torch.uint8, device=device)
+    # Kept alive by name until the call has read them.
+    table = array.array("Q", addresses), array.array("q", sizes), array.array("i", types)
+    src, num, typ = (a.buffer_info()[0] for a in table)
+    rest = (_buffer(norm, "norm", current)[0], *_buffer(workspace, "workspace", current),
+            _stream_of(stream, current if current >= 0 else 0))
+    if max_norm is None:
+        _check(lib.sa_grad_norm(src, num, typ, n, *rest), "sa_grad_norm")
+    else:
+        _check(lib.sa_clip_grad_norm(src, None if targets is None else targets.buffer_info()[0], num, typ,
+                                     n, max_norm, *rest), "sa_clip_grad_norm")
+    return norm
 
 
 def grad_norm(grads, norm=None, workspace=None, device=None, stream=None):
     """The global L2 norm of a list of bf16 and fp32 CUDA tensors
     (sa_grad_norm), as a device scalar."""
-    lib = load_library()
-    grads = list(grads)
-    addresses, sizes, types = _tensor_table(grads, "grads")
-    norm, buffers = _norm_buffers(lib, grads, norm, workspace, device)
-    _check(lib.sa_grad_norm(addresses, sizes, types, len(grads), *buffers, _stream_handle(stream)),
-           "sa_grad_norm")
-    return norm
+    return _clip(_torch(), load_library(), grads, None, None, norm, workspace, device, stream)
 
 
 def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, device=None,
@@ -1067,18 +1098,5 @@ def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, device=
     global norm (sa_clip_grad_norm), in place or into the tensors of `out`,
     and returns the norm before it as a device scalar.  Where the norm is not
     finite the values stay as they are."""
-    lib = load_library()
-    grads = list(grads)
-    addresses, sizes, types = _tensor_table(grads, "grads")
-    targets = None
-    if out is not None:
-        out = list(out)
-        if len(out) != len(grads) or any(o.shape != g.shape or o.dtype != g.dtype
-                                         for o, g in zip(out, grads)):
-            raise ValueError("out must match grads in number, shapes and types")
-        targets = _tensor_table(out, "out")[0]
-        _on_current_device(*out)
-    norm, buffers = _norm_buffers(lib, grads, norm, workspace, device)
-    _check(lib.sa_clip_grad_norm(addresses, targets, sizes, types, len(grads), float(max_norm),
-                                 *buffers, _stream_handle(stream)), "sa_clip_grad_norm")
-    return norm
+    return _clip(_torch(), load_library(), grads, float(max_norm), out, norm, workspace, device,
+                 stream)

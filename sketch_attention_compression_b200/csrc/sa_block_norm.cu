@@ -27,12 +27,14 @@
 // column sums stay in registers over the rows of a persistent block.  R is
 // the power of two that covers d: up to 32, several rows share a warp or
 // block and reduce by shuffles; above, one block holds one row and reduces
-// through shared memory with one barrier per reduction.  The next row's
-// operands are loaded before the current row is reduced, to keep loads in
-// flight across the reductions.  Rows whose width or address does not allow
-// 16-byte accesses use the same code with single-element loads at columns
-// R apart, so that neighbouring threads read neighbouring elements.
+// through shared memory with one barrier per reduction.  Rows whose width or
+// address does not allow 16-byte accesses use the same code with
+// single-element loads at columns R apart, so that neighbouring threads read
+// neighbouring elements.
 #include <cuda_bf16.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "sa.h"
 #include "sa_internal.h"
@@ -42,7 +44,8 @@ namespace sa {
 namespace {
 
 constexpr int kMaxNormWidth = 8192;
-constexpr int kMaxNormRows = 2;  // 8-column groups per thread at most
+constexpr int kMaxDevices = 64;
+constexpr int kCols = 8;         // columns per thread and group
 
 struct NormArgs {
   const void *x, *y, *z;        // forward: residual, block, gate; backward: r, block, gate
@@ -57,66 +60,127 @@ struct NormArgs {
   float eps, inv_d;
 };
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
-__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
-__device__ __forceinline__ void from_f(float v, uint16_t& o) {
-  o = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+// Rows in flight.  A thread copies its 8 neighbouring columns of every operand
+// of its next D rows into slots of shared memory that it alone reads (16-byte
+// asynchronous copies, no barrier), so that the bytes in flight, which the
+// bandwidth follows here, do not cost registers: 36 KB per SM in registers
+// gave 304 us for the backward over 400K x 128, see the kernels.  Rows that
+// do not allow 16-byte accesses go through registers, one row ahead.
+template <class T>
+__host__ __device__ constexpr int units() { return kCols * static_cast<int>(sizeof(T)) / 16; }
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Eight columns of one operand, as loaded.
-template <class T, bool VEC>
-struct Frag {
-  T v[8];
-  __device__ __forceinline__ void load(const T* row, int l, int j, int R, int d) {
-    if constexpr (VEC) {
-      const int c = (l + j * R) * 8;
-      if (c < d) {
-        const uint4* p = reinterpret_cast<const uint4*>(row + c);
-        uint4* q = reinterpret_cast<uint4*>(v);
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+
+template <class T, int R, int NV, int TT, bool VEC>
+struct Operand {
+  T v[VEC ? 1 : NV][VEC ? 1 : kCols];  // the register path's next row
+  // Starts the copy of a row into the slots at `slot` (stride: 16 bytes per
+  // thread of the block), or loads it.
+  __device__ __forceinline__ void fetch(const void* base, int64_t offset, uint32_t slot, int l, int d) {
+    const T* row = static_cast<const T*>(base) + offset;
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) q[i] = p[i];
-        return;
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (VEC) {
+        const int c = (l + j * R) * kCols;
+        if (c < d) {
+#pragma unroll
+          for (int i = 0; i < units<T>(); ++i)
+            copy_async(slot + (j * units<T>() + i) * TT * 16, row + c + i * (16 / static_cast<int>(sizeof(T))));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) {
+          const int c = l + R * (j * kCols + e);
+          v[j][e] = c < d ? row[c] : T(0);
+        }
       }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = l + R * (j * 8 + e);
-      v[e] = (!VEC && c < d) ? row[c] : T(0);
     }
   }
-  __device__ __forceinline__ void store(T* row, int l, int j, int R, int d) const {
-    if constexpr (VEC) {
-      const int c = (l + j * R) * 8;
-      if (c < d) {
-        uint4* p = reinterpret_cast<uint4*>(row + c);
-        const uint4* q = reinterpret_cast<const uint4*>(v);
+  __device__ __forceinline__ void take(bool use, uint32_t slot, int l, int d, float (&out)[NV][kCols]) const {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) p[i] = q[i];
-      }
-    } else {
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (VEC) {
+        if (use && (l + j * R) * kCols < d) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = l + R * (j * 8 + e);
-        if (c < d) row[c] = v[e];
+          for (int i = 0; i < units<T>(); ++i) {
+            const uint4 w = ld_shared_v4u(slot + (j * units<T>() + i) * TT * 16);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (sizeof(T) == 2) {
+                out[j][2 * k] = __uint_as_float(u[k] << 16);
+                out[j][2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+              } else {
+                out[j][4 * i + k] = __uint_as_float(u[k]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) out[j][e] = 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) out[j][e] = use ? to_f(v[j][e]) : 0.f;
       }
     }
   }
 };
 
+__device__ __forceinline__ void put8(float* row, const float (&v)[kCols]) {
+  reinterpret_cast<float4*>(row)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(row)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void put8(uint16_t* row, const float (&v)[kCols]) {
+  *reinterpret_cast<uint4*>(row) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void put1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put1(uint16_t* p, float v) {
+  *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+template <class T, int R, int NV, bool VEC>
+__device__ __forceinline__ void put_row(void* base, int64_t row, const float (&v)[NV][kCols], int l, int d) {
+  T* p = static_cast<T*>(base) + row * d;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if constexpr (VEC) {
+      const int c = (l + j * R) * kCols;
+      if (c < d) put8(p + c, v[j]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) {
+        const int c = l + R * (j * kCols + e);
+        if (c < d) put1(p + c, v[j][e]);
+      }
+    }
+  }
+}
+
 // Column of element e of group j (VEC: 8 neighbours; else R apart).
 template <bool VEC>
 __device__ __forceinline__ int column(int l, int j, int e, int R) {
-  return VEC ? (l + j * R) * 8 + e : l + R * (j * 8 + e);
+  return VEC ? (l + j * R) * kCols + e : l + R * (j * kCols + e);
 }
 
 template <bool VEC, int NV>
 __device__ __forceinline__ void load_params(const float* p, float fill, int l, int R, int d,
-                                            float (&out)[NV][8]) {
+                                            float (&out)[NV][kCols]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kCols; ++e) {
       const int c = column<VEC>(l, j, e, R);
       out[j][e] = c >= d ? 0.f : p != nullptr ? __ldg(p + c) : fill;
     }
@@ -170,111 +234,150 @@ __device__ __forceinline__ float gate_slope(float z, int kind, float& a) {
   return s * (1.f + z * (1.f - s));
 }
 
+// v - mean in the row's columns, 0 behind them.
+template <bool VEC, int R, int NV>
+__device__ __forceinline__ void subtract(float (&v)[NV][kCols], float mean, const NormArgs& a, int l) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < kCols; ++e)
+      v[j][e] = column<VEC>(l, j, VEC ? 0 : e, R) < a.d ? v[j][e] - mean : 0.f;
+}
+
 // In place: v -> (v - mean) with mean the row's (layer form); returns rstd.
 template <bool VEC, int R, int NV>
-__device__ __forceinline__ float centre(float (&v)[NV][8], const NormArgs& a, int l, float* buf,
+__device__ __forceinline__ float centre(float (&v)[NV][kCols], const NormArgs& a, int l, float* buf,
                                         int& phase) {
   if (a.layer) {
     float s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += v[j][e];
+      for (int e = 0; e < kCols; ++e) s[0] += v[j][e];
     row_sum<R, 1>(s, buf, phase);
-    const float mean = s[0] * a.inv_d;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[j][e] = column<VEC>(l, j, e, R) < a.d ? v[j][e] - mean : 0.f;
+    subtract<VEC, R, NV>(v, s[0] * a.inv_d, a, l);
   }
   float q[1] = {0.f};
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[0] = fmaf(v[j][e], v[j][e], q[0]);
+    for (int e = 0; e < kCols; ++e) q[0] = fmaf(v[j][e], v[j][e], q[0]);
   row_sum<R, 1>(q, buf, phase);
   return rsqrtf(fmaf(q[0], a.inv_d, a.eps));
+}
+
+// The same for two rows of values at once, with half as many reductions.
+template <bool VEC, int R, int NV>
+__device__ __forceinline__ void centre2(float (&v)[NV][kCols], float (&w)[NV][kCols], const NormArgs& a,
+                                        int l, float* buf, int& phase, float& rv, float& rw) {
+  if (a.layer) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) s[0] += v[j][e], s[1] += w[j][e];
+    row_sum<R, 2>(s, buf, phase);
+    subtract<VEC, R, NV>(v, s[0] * a.inv_d, a, l);
+    subtract<VEC, R, NV>(w, s[1] * a.inv_d, a, l);
+  }
+  float q[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) {
+      q[0] = fmaf(v[j][e], v[j][e], q[0]);
+      q[1] = fmaf(w[j][e], w[j][e], q[1]);
+    }
+  row_sum<R, 2>(q, buf, phase);
+  rv = rsqrtf(fmaf(q[0], a.inv_d, a.eps));
+  rw = rsqrtf(fmaf(q[1], a.inv_d, a.eps));
 }
 
 template <int R>
 __host__ __device__ constexpr int norm_threads() { return R <= 256 ? (R <= 128 ? 128 : 256) : R; }
 
+// Stages of the ring: up to `most`, within 200 KB for a block.
+template <int SLOTS, int T, bool VEC>
+__host__ __device__ constexpr int ring_stages(int most) {
+  const int fit = 200 * 1024 / (SLOTS * T * 16);
+  return !VEC ? 1 : fit < 1 ? 1 : fit < most ? fit : most;
+}
+template <class TB, class TR, int R, int NV, bool VEC, bool BACK>
+struct NormPlan {
+  static constexpr int T = norm_threads<R>();
+  static constexpr int G = R > 32 ? 1 : T / R;  // rows per block (R > 32: R == T)
+  static constexpr int kSlots = NV * (BACK ? 2 * units<TR>() + 3 * units<TB>() : units<TR>() + 2 * units<TB>());
+  static constexpr int D = ring_stages<kSlots, T, VEC>(BACK ? 3 : 4);
+  static constexpr int kSmem = VEC ? D * kSlots * T * 16 : 0;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(R <= 32 || R == T, "one row per block above a warp");
+};
+
 template <class TB, class TR, int R, int NV, bool VEC>
 __global__ void __launch_bounds__(norm_threads<R>())
     block_norm_forward_kernel(const NormArgs a) {
-  constexpr int T = norm_threads<R>();
-  constexpr int G = R > 32 ? 1 : T / R;  // rows per block (R > 32: R == T)
-  static_assert(R <= 32 || R == T, "one row per block above a warp");
+  using Pl = NormPlan<TB, TR, R, NV, VEC, false>;
+  constexpr int T = Pl::T, G = Pl::G, D = Pl::D;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float buf[4 * (T / 32)];
   const int l = R > 32 ? threadIdx.x : threadIdx.x % R;
   const int grp = R > 32 ? 0 : threadIdx.x / R;
   int phase = 0;
-  float g1[NV][8], b1[NV][8], rs[NV][8], g2[NV][8], b2[NV][8];
+  float g1[NV][kCols], b1[NV][kCols], rs[NV][kCols], g2[NV][kCols], b2[NV][kCols];
   load_params<VEC, NV>(a.g1, 1.f, l, R, a.d, g1);
   load_params<VEC, NV>(a.b1, 0.f, l, R, a.d, b1);
   load_params<VEC, NV>(a.rs, 1.f, l, R, a.d, rs);
   load_params<VEC, NV>(a.g2, 1.f, l, R, a.d, g2);
   load_params<VEC, NV>(a.b2, 0.f, l, R, a.d, b2);
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-  Frag<TR, VEC> fx[NV];
-  Frag<TB, VEC> fy[NV], fz[NV];
-  auto fetch = [&](int64_t row) {
-    if (row >= a.rows) return;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      fx[j].load(static_cast<const TR*>(a.x) + row * a.ldx, l, j, R, a.d);
-      if (a.y != nullptr) fy[j].load(static_cast<const TB*>(a.y) + row * a.ldy, l, j, R, a.d);
-      if (a.z != nullptr) fz[j].load(static_cast<const TB*>(a.z) + row * a.ldz, l, j, R, a.d);
+  Operand<TR, R, NV, T, VEC> ox;
+  Operand<TB, R, NV, T, VEC> oy, oz;
+  constexpr int kY = NV * units<TR>() * T * 16, kZ = kY + NV * units<TB>() * T * 16;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  auto fetch = [&](int stage, int64_t row) {
+    if (row < a.rows) {
+      const uint32_t slot = mine + stage * (Pl::kSlots * T * 16);
+      ox.fetch(a.x, row * a.ldx, slot, l, a.d);
+      if (a.y != nullptr) oy.fetch(a.y, row * a.ldy, slot + kY, l, a.d);
+      if (a.z != nullptr) oz.fetch(a.z, row * a.ldz, slot + kZ, l, a.d);
     }
+    if (VEC) copy_commit();
   };
-  // Groups past the last row go through the same reductions on old values
-  // and store nothing.
-  fetch(static_cast<int64_t>(blockIdx.x) * G + grp);
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < a.rows; row0 += step) {
-    const int64_t row = row0 + grp;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + grp;
+#pragma unroll
+  for (int i = 0; i < D; ++i) fetch(i, row + i * step);
+  int stage = 0;
+  // Groups past the last row go through the same reductions on zeros and
+  // store nothing.
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < a.rows; row0 += step, row += step) {
     const bool live = row < a.rows;
-    float x[NV][8], y[NV][8], z[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[j][e] = to_f(fx[j].v[e]);
-        y[j][e] = a.y != nullptr ? to_f(fy[j].v[e]) : 0.f;
-        z[j][e] = a.z != nullptr ? to_f(fz[j].v[e]) : 0.f;
-      }
-    fetch(row + step);
+    float x[NV][kCols], y[NV][kCols], z[NV][kCols];
+    if (VEC) copy_wait<D - 1>();
+    const uint32_t slot = mine + stage * (Pl::kSlots * T * 16);
+    ox.take(live, slot, l, a.d, x);
+    oy.take(live && a.y != nullptr, slot + kY, l, a.d, y);
+    oz.take(live && a.z != nullptr, slot + kZ, l, a.d, z);
+    fetch(stage, row + D * step);
+    stage = stage + 1 == D ? 0 : stage + 1;
     if (a.y != nullptr) {
       const float ry = a.g1 != nullptr ? centre<VEC, R, NV>(y, a, l, buf, phase) : 1.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kCols; ++e) {
           const float n = fmaf(y[j][e] * ry, g1[j][e], b1[j][e]);
           const float act = a.z != nullptr ? gate_value(z[j][e], a.gate_kind) : 1.f;
           x[j][e] = fmaf(rs[j][e] * act, n, x[j][e]);
         }
-      if (a.o1 != nullptr && live) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          Frag<TR, VEC> o;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) from_f(x[j][e], o.v[e]);
-          o.store(static_cast<TR*>(a.o1) + row * a.d, l, j, R, a.d);
-        }
-      }
+      if (a.o1 != nullptr && live) put_row<TR, R, NV, VEC>(a.o1, row, x, l, a.d);
     }
     if (a.o2 != nullptr) {
       const float rr = centre<VEC, R, NV>(x, a, l, buf, phase);
-      if (live) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          Frag<TB, VEC> o;
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) from_f(fmaf(x[j][e] * rr, g2[j][e], b2[j][e]), o.v[e]);
-          o.store(static_cast<TB*>(a.o2) + row * a.d, l, j, R, a.d);
-        }
-      }
+        for (int e = 0; e < kCols; ++e) x[j][e] = fmaf(x[j][e] * rr, g2[j][e], b2[j][e]);
+      if (live) put_row<TB, R, NV, VEC>(a.o2, row, x, l, a.d);
     }
   }
 }
@@ -282,70 +385,79 @@ __global__ void __launch_bounds__(norm_threads<R>())
 template <class TB, class TR, int R, int NV, bool VEC>
 __global__ void __launch_bounds__(norm_threads<R>())
     block_norm_backward_kernel(const NormArgs a) {
-  constexpr int T = norm_threads<R>();
-  constexpr int G = R > 32 ? 1 : T / R;
-  static_assert(R <= 32 || R == T, "one row per block above a warp");
+  using Pl = NormPlan<TB, TR, R, NV, VEC, true>;
+  constexpr int T = Pl::T, G = Pl::G, D = Pl::D;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float buf[4 * (T / 32)];
-  __shared__ float red[G > 1 ? T * 8 : 1];
+  __shared__ float red[G > 1 ? T * kCols : 1];
   const int l = R > 32 ? threadIdx.x : threadIdx.x % R;
   const int grp = R > 32 ? 0 : threadIdx.x / R;
   int phase = 0;
-  float g1[NV][8], b1[NV][8], rs[NV][8], g2[NV][8];
+  float g1[NV][kCols], b1[NV][kCols], rs[NV][kCols], g2[NV][kCols];
   load_params<VEC, NV>(a.g1, 1.f, l, R, a.d, g1);
   load_params<VEC, NV>(a.b1, 0.f, l, R, a.d, b1);
   load_params<VEC, NV>(a.rs, 1.f, l, R, a.d, rs);
   load_params<VEC, NV>(a.g2, 1.f, l, R, a.d, g2);
-  float acc[5][NV][8];  // dg1, db1, drs, dg2, db2
+  float acc[5][NV][kCols];  // dg1, db1, drs, dg2, db2
 #pragma unroll
   for (int i = 0; i < 5; ++i)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[i][j][e] = 0.f;
+      for (int e = 0; e < kCols; ++e) acc[i][j][e] = 0.f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-  Frag<TR, VEC> fx[NV], fdr[NV];
-  Frag<TB, VEC> fy[NV], fz[NV], fdu[NV];
-  auto fetch = [&](int64_t row) {
-    if (row >= a.rows) return;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
+  Operand<TR, R, NV, T, VEC> ox, odr;
+  Operand<TB, R, NV, T, VEC> oy, oz, odu;
+  constexpr int kDr = NV * units<TR>() * T * 16, kY = 2 * kDr, kZ = kY + NV * units<TB>() * T * 16,
+                kDu = kZ + NV * units<TB>() * T * 16;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  auto fetch = [&](int stage, int64_t row) {
+    if (row < a.rows) {
+      const uint32_t slot = mine + stage * (Pl::kSlots * T * 16);
       if (a.du != nullptr) {
-        fx[j].load(static_cast<const TR*>(a.x) + row * a.ldx, l, j, R, a.d);
-        fdu[j].load(static_cast<const TB*>(a.du) + row * a.lddu, l, j, R, a.d);
+        ox.fetch(a.x, row * a.ldx, slot, l, a.d);
+        odu.fetch(a.du, row * a.lddu, slot + kDu, l, a.d);
       }
-      if (a.y != nullptr) fy[j].load(static_cast<const TB*>(a.y) + row * a.ldy, l, j, R, a.d);
-      if (a.z != nullptr) fz[j].load(static_cast<const TB*>(a.z) + row * a.ldz, l, j, R, a.d);
-      if (a.dr != nullptr) fdr[j].load(static_cast<const TR*>(a.dr) + row * a.lddr, l, j, R, a.d);
+      if (a.y != nullptr) oy.fetch(a.y, row * a.ldy, slot + kY, l, a.d);
+      if (a.z != nullptr) oz.fetch(a.z, row * a.ldz, slot + kZ, l, a.d);
+      if (a.dr != nullptr) odr.fetch(a.dr, row * a.lddr, slot + kDr, l, a.d);
     }
+    if (VEC) copy_commit();
   };
-  fetch(static_cast<int64_t>(blockIdx.x) * G + grp);
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < a.rows; row0 += step) {
-    const int64_t row = row0 + grp;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + grp;
+#pragma unroll
+  for (int i = 0; i < D; ++i) fetch(i, row + i * step);
+  int stage = 0;
+  // Groups past the last row go through the same reductions on zeros, which
+  // add nothing to the sums, and store nothing.
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < a.rows; row0 += step, row += step) {
     const bool live = row < a.rows;
-    float x[NV][8], dx[NV][8], y[NV][8], z[NV][8], h[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[j][e] = a.du != nullptr ? to_f(fx[j].v[e]) : 0.f;
-        h[j][e] = live && a.du != nullptr ? to_f(fdu[j].v[e]) : 0.f;
-        y[j][e] = a.y != nullptr ? to_f(fy[j].v[e]) : 0.f;
-        z[j][e] = a.z != nullptr ? to_f(fz[j].v[e]) : 0.f;
-        dx[j][e] = live && a.dr != nullptr ? to_f(fdr[j].v[e]) : 0.f;
-      }
-    fetch(row + step);
+    float x[NV][kCols], dx[NV][kCols], y[NV][kCols], z[NV][kCols], h[NV][kCols];
+    if (VEC) copy_wait<D - 1>();
+    const uint32_t slot = mine + stage * (Pl::kSlots * T * 16);
+    ox.take(live && a.du != nullptr, slot, l, a.d, x);
+    odu.take(live && a.du != nullptr, slot + kDu, l, a.d, h);
+    oy.take(live && a.y != nullptr, slot + kY, l, a.d, y);
+    oz.take(live && a.z != nullptr, slot + kZ, l, a.d, z);
+    odr.take(live && a.dr != nullptr, slot + kDr, l, a.d, dx);
+    fetch(stage, row + D * step);
+    stage = stage + 1 == D ? 0 : stage + 1;
+    float rr = 1.f, ry = 1.f;
+    if (a.du != nullptr && a.g1 != nullptr)
+      centre2<VEC, R, NV>(x, y, a, l, buf, phase, rr, ry);
+    else if (a.du != nullptr)
+      rr = centre<VEC, R, NV>(x, a, l, buf, phase);
+    else if (a.g1 != nullptr)
+      ry = centre<VEC, R, NV>(y, a, l, buf, phase);
     if (a.du != nullptr) {
-      const float rr = centre<VEC, R, NV>(x, a, l, buf, phase);
       float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kCols; ++e) {
           const float xh = x[j][e] * rr, du = h[j][e];
-          if (live) {
-            acc[3][j][e] = fmaf(du, xh, acc[3][j][e]);
-            acc[4][j][e] += du;
-          }
+          acc[3][j][e] = fmaf(du, xh, acc[3][j][e]);
+          acc[4][j][e] += du;
           x[j][e] = xh;
           h[j][e] = du * g2[j][e];
           s[0] = fmaf(h[j][e], xh, s[0]);
@@ -356,70 +468,42 @@ __global__ void __launch_bounds__(norm_threads<R>())
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < kCols; ++e)
           dx[j][e] = fmaf(rr, h[j][e] - c2 - x[j][e] * c1, dx[j][e]);
     }
-    if (a.o1 != nullptr && live) {
+    if (a.o1 != nullptr && live) put_row<TR, R, NV, VEC>(a.o1, row, dx, l, a.d);
+    if (a.y == nullptr) continue;
+    float s[2] = {0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        Frag<TR, VEC> o;
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) from_f(dx[j][e], o.v[e]);
-        o.store(static_cast<TR*>(a.o1) + row * a.d, l, j, R, a.d);
+      for (int e = 0; e < kCols; ++e) {
+        const float yh = y[j][e] * ry;
+        const float n = fmaf(yh, g1[j][e], b1[j][e]);
+        float act = 1.f, slope = 0.f;
+        if (a.z != nullptr) slope = gate_slope(z[j][e], a.gate_kind, act);
+        const float ds = dx[j][e] * rs[j][e];
+        const float dn = ds * act;
+        z[j][e] = ds * n * slope;  // dz
+        acc[2][j][e] = fmaf(dx[j][e] * act, n, acc[2][j][e]);
+        acc[0][j][e] = fmaf(dn, yh, acc[0][j][e]);
+        acc[1][j][e] += dn;
+        const float p = dn * g1[j][e];
+        y[j][e] = yh;
+        dx[j][e] = p;
+        s[0] = fmaf(p, yh, s[0]);
+        s[1] += p;
       }
-    }
-    if (a.y != nullptr) {
-      const float ry = a.g1 != nullptr ? centre<VEC, R, NV>(y, a, l, buf, phase) : 1.f;
-      float s[2] = {0.f, 0.f};
+    if (a.o3 != nullptr && live) put_row<TB, R, NV, VEC>(a.o3, row, z, l, a.d);
+    if (a.g1 != nullptr) {
+      row_sum<R, 2>(s, buf, phase);
+      const float c1 = s[0] * a.inv_d, c2 = a.layer ? s[1] * a.inv_d : 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float yh = y[j][e] * ry;
-          const float n = fmaf(yh, g1[j][e], b1[j][e]);
-          float act = 1.f, slope = 0.f;
-          if (a.z != nullptr) slope = gate_slope(z[j][e], a.gate_kind, act);
-          const float ds = dx[j][e] * rs[j][e];
-          const float dn = ds * act;
-          z[j][e] = ds * n * slope;  // dz
-          if (live) {
-            acc[2][j][e] = fmaf(dx[j][e] * act, n, acc[2][j][e]);
-            acc[0][j][e] = fmaf(dn, yh, acc[0][j][e]);
-            acc[1][j][e] += dn;
-          }
-          const float p = dn * g1[j][e];
-          y[j][e] = yh;
-          dx[j][e] = p;
-          s[0] = fmaf(p, yh, s[0]);
-          s[1] += p;
-        }
-      if (a.o3 != nullptr && live) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          Frag<TB, VEC> o;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) from_f(z[j][e], o.v[e]);
-          o.store(static_cast<TB*>(a.o3) + row * a.d, l, j, R, a.d);
-        }
-      }
-      if (a.g1 != nullptr) {
-        row_sum<R, 2>(s, buf, phase);
-        const float c1 = s[0] * a.inv_d, c2 = a.layer ? s[1] * a.inv_d : 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dx[j][e] = ry * (dx[j][e] - c2 - y[j][e] * c1);
-      }
-      if (a.o2 != nullptr && live) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          Frag<TB, VEC> o;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) from_f(dx[j][e], o.v[e]);
-          o.store(static_cast<TB*>(a.o2) + row * a.d, l, j, R, a.d);
-        }
-      }
+        for (int e = 0; e < kCols; ++e) dx[j][e] = ry * (dx[j][e] - c2 - y[j][e] * c1);
     }
+    if (a.o2 != nullptr && live) put_row<TB, R, NV, VEC>(a.o2, row, dx, l, a.d);
   }
   if (!a.sums) return;
   // The block's column sums: its row groups in ascending order.
@@ -431,11 +515,11 @@ __global__ void __launch_bounds__(norm_threads<R>())
       if constexpr (G > 1) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) red[e * T + threadIdx.x] = acc[i][j][e];
+        for (int e = 0; e < kCols; ++e) red[e * T + threadIdx.x] = acc[i][j][e];
         __syncthreads();
         if (grp == 0) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < kCols; ++e) {
             float s = 0.f;
             for (int g = 0; g < G; ++g) s += red[e * T + g * R + l];
             const int c = column<VEC>(l, j, e, R);
@@ -444,7 +528,7 @@ __global__ void __launch_bounds__(norm_threads<R>())
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kCols; ++e) {
           const int c = column<VEC>(l, j, e, R);
           if (c < a.d) part[i * a.d + c] = acc[i][j][e];
         }
@@ -480,40 +564,51 @@ __global__ void __launch_bounds__(256) block_norm_sums_kernel(const float* part,
 // columns per thread, 4 to 512; above 4096 columns two groups.
 int row_threads(int d) {
   int r = 4;
-  while (r * 8 < d && r < 512) r *= 2;
+  while (r * kCols < d && r < 512) r *= 2;
   return r == 64 ? 128 : r;  // a block of one row has at least 128 threads
 }
 
-template <class TB, class TR, int R, int NV, bool VEC>
-cudaError_t launch_norm(const NormArgs& a, bool backward, int sms, int* blocks, cudaStream_t st) {
-  constexpr int T = norm_threads<R>();
-  constexpr int G = R > 32 ? 1 : T / R;
-  auto kernel = backward ? block_norm_backward_kernel<TB, TR, R, NV, VEC>
-                         : block_norm_forward_kernel<TB, TR, R, NV, VEC>;
-  int per_sm = 0;
-  cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, T, 0);
+template <class TB, class TR, int R, int NV, bool VEC, bool BACK>
+cudaError_t launch_norm(const NormArgs& a, int sms, int* blocks, cudaStream_t st) {
+  using Pl = NormPlan<TB, TR, R, NV, VEC, BACK>;
+  void (*kernel)(NormArgs);
+  if constexpr (BACK) kernel = block_norm_backward_kernel<TB, TR, R, NV, VEC>;
+  else kernel = block_norm_forward_kernel<TB, TR, R, NV, VEC>;
+  // Set and asked once per device: blocks that fit an SM.
+  static std::atomic<int> resident[kMaxDevices];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  const int64_t need = (a.rows + G - 1) / G;
-  const int64_t most = static_cast<int64_t>(sms) * (per_sm < 1 ? 1 : per_sm);
+  int per_sm = dev < kMaxDevices ? resident[dev].load(std::memory_order_relaxed) : 0;
+  if (per_sm == 0) {
+    if (Pl::kSmem > 0)
+      err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::kSmem);
+    if (err == cudaSuccess)
+      err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Pl::T, Pl::kSmem);
+    if (err != cudaSuccess) return err;
+    if (per_sm < 1) per_sm = 1;
+    if (dev < kMaxDevices) resident[dev].store(per_sm, std::memory_order_relaxed);
+  }
+  const int64_t need = (a.rows + Pl::G - 1) / Pl::G;
+  const int64_t most = static_cast<int64_t>(sms) * per_sm;
   *blocks = static_cast<int>(need < most ? need : most);
-  kernel<<<static_cast<unsigned>(*blocks), T, 0, st>>>(a);
+  kernel<<<static_cast<unsigned>(*blocks), Pl::T, Pl::kSmem, st>>>(a);
   return cudaGetLastError();
 }
 
-template <class TB, class TR, bool VEC>
-cudaError_t dispatch_width(const NormArgs& a, bool backward, int sms, int* blocks,
-                           cudaStream_t st) {
+template <class TB, class TR, bool VEC, bool BACK>
+cudaError_t dispatch_width(const NormArgs& a, int sms, int* blocks, cudaStream_t st) {
   switch (row_threads(a.d)) {
-    case 4: return launch_norm<TB, TR, 4, 1, VEC>(a, backward, sms, blocks, st);
-    case 8: return launch_norm<TB, TR, 8, 1, VEC>(a, backward, sms, blocks, st);
-    case 16: return launch_norm<TB, TR, 16, 1, VEC>(a, backward, sms, blocks, st);
-    case 32: return launch_norm<TB, TR, 32, 1, VEC>(a, backward, sms, blocks, st);
-    case 128: return launch_norm<TB, TR, 128, 1, VEC>(a, backward, sms, blocks, st);
-    case 256: return launch_norm<TB, TR, 256, 1, VEC>(a, backward, sms, blocks, st);
-    default:
-      return a.d <= 4096 ? launch_norm<TB, TR, 512, 1, VEC>(a, backward, sms, blocks, st)
-                         : launch_norm<TB, TR, 512, kMaxNormRows, VEC>(a, backward, sms, blocks, st);
+    case 4: return launch_norm<TB, TR, 4, 1, VEC, BACK>(a, sms, blocks, st);
+    case 8: return launch_norm<TB, TR, 8, 1, VEC, BACK>(a, sms, blocks, st);
+    case 16: return launch_norm<TB, TR, 16, 1, VEC, BACK>(a, sms, blocks, st);
+    case 32: return launch_norm<TB, TR, 32, 1, VEC, BACK>(a, sms, blocks, st);
+    case 128: return launch_norm<TB, TR, 128, 1, VEC, BACK>(a, sms, blocks, st);
+    case 256: return launch_norm<TB, TR, 256, 1, VEC, BACK>(a, sms, blocks, st);
+    default: break;
   }
+  return a.d <= 4096 ? launch_norm<TB, TR, 512, 1, VEC, BACK>(a, sms, blocks, st)
+                     : launch_norm<TB, TR, 512, 2, VEC, BACK>(a, sms, blocks, st);
 }
 
 bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -533,17 +628,22 @@ bool vector_rows(const NormArgs& a, size_t er, size_t eb) {
   return true;
 }
 
+template <class TB, class TR>
+cudaError_t dispatch_types(const NormArgs& a, bool vec, bool backward, int sms, int* blocks,
+                           cudaStream_t st) {
+  if (backward)
+    return vec ? dispatch_width<TB, TR, true, true>(a, sms, blocks, st)
+               : dispatch_width<TB, TR, false, true>(a, sms, blocks, st);
+  return vec ? dispatch_width<TB, TR, true, false>(a, sms, blocks, st)
+             : dispatch_width<TB, TR, false, false>(a, sms, blocks, st);
+}
+
 cudaError_t dispatch(const NormArgs& a, sa_dtype tr, sa_dtype tb, bool backward, int sms,
                      int* blocks, cudaStream_t st) {
   const bool vec = vector_rows(a, tr == SA_BF16 ? 2 : 4, tb == SA_BF16 ? 2 : 4);
-  if (tb == SA_FP32)
-    return vec ? dispatch_width<float, float, true>(a, backward, sms, blocks, st)
-               : dispatch_width<float, float, false>(a, backward, sms, blocks, st);
-  if (tr == SA_FP32)
-    return vec ? dispatch_width<uint16_t, float, true>(a, backward, sms, blocks, st)
-               : dispatch_width<uint16_t, float, false>(a, backward, sms, blocks, st);
-  return vec ? dispatch_width<uint16_t, uint16_t, true>(a, backward, sms, blocks, st)
-             : dispatch_width<uint16_t, uint16_t, false>(a, backward, sms, blocks, st);
+  if (tb == SA_FP32) return dispatch_types<float, float>(a, vec, backward, sms, blocks, st);
+  if (tr == SA_FP32) return dispatch_types<uint16_t, float>(a, vec, backward, sms, blocks, st);
+  return dispatch_types<uint16_t, uint16_t>(a, vec, backward, sms, blocks, st);
 }
 
 // Most blocks the backward pass may launch on a device of `sms` SMs (its
