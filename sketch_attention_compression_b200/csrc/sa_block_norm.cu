@@ -46,6 +46,7 @@ namespace {
 constexpr int kMaxNormWidth = 8192;
 constexpr int kMaxDevices = 64;
 constexpr int kCols = 8;         // columns per thread and group
+constexpr int kPairs = kCols / 2;  // as pairs, for packed fp32 arithmetic
 
 struct NormArgs {
   const void *x, *y, *z;        // forward: residual, block, gate; backward: r, block, gate
@@ -81,6 +82,17 @@ __device__ __forceinline__ void copy_wait() {
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 
+// Two bf16 as a pair of fp32.
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint64_t both(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
+}
+
 template <class T, int R, int NV, int TT, bool VEC>
 struct Operand {
   T v[VEC ? 1 : NV][VEC ? 1 : kCols];  // the register path's next row
@@ -106,7 +118,7 @@ struct Operand {
       }
     }
   }
-  __device__ __forceinline__ void take(bool use, uint32_t slot, int l, int d, float (&out)[NV][kCols]) const {
+  __device__ __forceinline__ void take(bool use, uint32_t slot, int l, int d, uint64_t (&out)[NV][kPairs]) const {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if constexpr (VEC) {
@@ -114,36 +126,38 @@ struct Operand {
 #pragma unroll
           for (int i = 0; i < units<T>(); ++i) {
             const uint4 w = ld_shared_v4u(slot + (j * units<T>() + i) * TT * 16);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if constexpr (sizeof(T) == 2) {
-                out[j][2 * k] = __uint_as_float(u[k] << 16);
-                out[j][2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-              } else {
-                out[j][4 * i + k] = __uint_as_float(u[k]);
-              }
+            if constexpr (sizeof(T) == 2) {
+              out[j][0] = widen(w.x), out[j][1] = widen(w.y), out[j][2] = widen(w.z), out[j][3] = widen(w.w);
+            } else {
+              out[j][2 * i] = f2_pack(__uint_as_float(w.x), __uint_as_float(w.y));
+              out[j][2 * i + 1] = f2_pack(__uint_as_float(w.z), __uint_as_float(w.w));
             }
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) out[j][e] = 0.f;
+          for (int e = 0; e < kPairs; ++e) out[j][e] = 0ull;
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) out[j][e] = use ? to_f(v[j][e]) : 0.f;
+        for (int e = 0; e < kPairs; ++e)
+          out[j][e] = use ? f2_pack(to_f(v[j][2 * e]), to_f(v[j][2 * e + 1])) : 0ull;
       }
     }
   }
 };
 
-__device__ __forceinline__ void put8(float* row, const float (&v)[kCols]) {
-  reinterpret_cast<float4*>(row)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(row)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void put8(float* row, const uint64_t (&v)[kPairs]) {
+  ulonglong2* p = reinterpret_cast<ulonglong2*>(row);
+  p[0] = make_ulonglong2(v[0], v[1]);
+  p[1] = make_ulonglong2(v[2], v[3]);
 }
-__device__ __forceinline__ void put8(uint16_t* row, const float (&v)[kCols]) {
-  *reinterpret_cast<uint4*>(row) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint32_t narrow(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ void put8(uint16_t* row, const uint64_t (&v)[kPairs]) {
+  *reinterpret_cast<uint4*>(row) = make_uint4(narrow(v[0]), narrow(v[1]), narrow(v[2]), narrow(v[3]));
 }
 __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put1(uint16_t* p, float v) {
@@ -151,7 +165,8 @@ __device__ __forceinline__ void put1(uint16_t* p, float v) {
 }
 
 template <class T, int R, int NV, bool VEC>
-__device__ __forceinline__ void put_row(void* base, int64_t row, const float (&v)[NV][kCols], int l, int d) {
+__device__ __forceinline__ void put_row(void* base, int64_t row, const uint64_t (&v)[NV][kPairs], int l,
+                                        int d) {
   T* p = static_cast<T*>(base) + row * d;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -162,7 +177,9 @@ __device__ __forceinline__ void put_row(void* base, int64_t row, const float (&v
 #pragma unroll
       for (int e = 0; e < kCols; ++e) {
         const int c = l + R * (j * kCols + e);
-        if (c < d) put1(p + c, v[j][e]);
+        float f[2];
+        f2_unpack(v[j][e / 2], f[0], f[1]);
+        if (c < d) put1(p + c, f[e % 2]);
       }
     }
   }
@@ -176,14 +193,13 @@ __device__ __forceinline__ int column(int l, int j, int e, int R) {
 
 template <bool VEC, int NV>
 __device__ __forceinline__ void load_params(const float* p, float fill, int l, int R, int d,
-                                            float (&out)[NV][kCols]) {
+                                            uint64_t (&out)[NV][kPairs]) {
+  auto at = [&](int c) { return c >= d ? 0.f : p != nullptr ? __ldg(p + c) : fill; };
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < kCols; ++e) {
-      const int c = column<VEC>(l, j, e, R);
-      out[j][e] = c >= d ? 0.f : p != nullptr ? __ldg(p + c) : fill;
-    }
+    for (int e = 0; e < kPairs; ++e)
+      out[j][e] = f2_pack(at(column<VEC>(l, j, 2 * e, R)), at(column<VEC>(l, j, 2 * e + 1, R)));
 }
 
 // Sums of K values over the R threads of a row (R <= 32: within the warp; R
@@ -214,80 +230,104 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* buf, int& phase) {
   }
 }
 
-// act(z) and act'(z).  kind 0: z, 1: sigmoid(z), 2: z sigmoid(z).
-__device__ __forceinline__ float gate_value(float z, int kind) {
-  if (kind == 0) return z;
-  const float s = __fdividef(1.f, 1.f + __expf(-z));
-  return kind == 1 ? s : z * s;
+// 1 / (1 + exp(-z)) of a pair.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
+  float a, b;
+  f2_unpack(f2_mul(z, both(-1.4426950408889634f)), a, b);
+  f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), both(1.f)), a, b);
+  return f2_pack(rcp_approx(a), rcp_approx(b));
 }
-__device__ __forceinline__ float gate_slope(float z, int kind, float& a) {
-  if (kind == 0) {
-    a = z;
-    return 1.f;
-  }
-  const float s = __fdividef(1.f, 1.f + __expf(-z));
-  if (kind == 1) {
-    a = s;
-    return s * (1.f - s);
-  }
-  a = z * s;
-  return s * (1.f + z * (1.f - s));
-}
-
-// v - mean in the row's columns, 0 behind them.
-template <bool VEC, int R, int NV>
-__device__ __forceinline__ void subtract(float (&v)[NV][kCols], float mean, const NormArgs& a, int l) {
+// act(z) in place.  kind 0: z, 1: sigmoid(z), 2: z sigmoid(z).
+template <int NV>
+__device__ __forceinline__ void gate_values(uint64_t (&z)[NV][kPairs], int kind) {
+  if (kind == 0) return;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < kCols; ++e)
-      v[j][e] = column<VEC>(l, j, VEC ? 0 : e, R) < a.d ? v[j][e] - mean : 0.f;
+    for (int e = 0; e < kPairs; ++e) {
+      const uint64_t s = sigmoid2(z[j][e]);
+      z[j][e] = kind == 1 ? s : f2_mul(z[j][e], s);
+    }
+}
+// act'(z), and act(z) in `act`.
+__device__ __forceinline__ uint64_t gate_slope(uint64_t z, int kind, uint64_t& act) {
+  const uint64_t one = both(1.f), minus = both(-1.f);
+  if (kind == 0) {
+    act = z;
+    return one;
+  }
+  const uint64_t s = sigmoid2(z), rest = f2_fma(minus, s, one);  // 1 - s
+  if (kind == 1) {
+    act = s;
+    return f2_mul(s, rest);
+  }
+  act = f2_mul(z, s);
+  return f2_mul(s, f2_fma(z, rest, one));
+}
+
+// v - mean in the row's columns; the columns behind them hold 0 and keep it.
+template <bool VEC, int R, int NV>
+__device__ __forceinline__ void subtract(uint64_t (&v)[NV][kPairs], float mean, const NormArgs& a, int l) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if constexpr (VEC) {
+      const uint64_t m = both((l + j * R) * kCols < a.d ? -mean : 0.f);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) v[j][e] = f2_add(v[j][e], m);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e)
+        v[j][e] = f2_add(v[j][e], f2_pack(column<VEC>(l, j, 2 * e, R) < a.d ? -mean : 0.f,
+                                          column<VEC>(l, j, 2 * e + 1, R) < a.d ? -mean : 0.f));
+    }
+  }
+}
+
+template <int NV>
+__device__ __forceinline__ float total(const uint64_t (&v)[NV][kPairs]) {
+  uint64_t s = 0ull;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) s = f2_add(s, v[j][e]);
+  return f2_sum(s);
+}
+template <int NV>
+__device__ __forceinline__ float total_squares(const uint64_t (&v)[NV][kPairs]) {
+  uint64_t s = 0ull;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) s = f2_fma(v[j][e], v[j][e], s);
+  return f2_sum(s);
 }
 
 // In place: v -> (v - mean) with mean the row's (layer form); returns rstd.
 template <bool VEC, int R, int NV>
-__device__ __forceinline__ float centre(float (&v)[NV][kCols], const NormArgs& a, int l, float* buf,
+__device__ __forceinline__ float centre(uint64_t (&v)[NV][kPairs], const NormArgs& a, int l, float* buf,
                                         int& phase) {
   if (a.layer) {
-    float s[1] = {0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < kCols; ++e) s[0] += v[j][e];
+    float s[1] = {total(v)};
     row_sum<R, 1>(s, buf, phase);
     subtract<VEC, R, NV>(v, s[0] * a.inv_d, a, l);
   }
-  float q[1] = {0.f};
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < kCols; ++e) q[0] = fmaf(v[j][e], v[j][e], q[0]);
+  float q[1] = {total_squares(v)};
   row_sum<R, 1>(q, buf, phase);
   return rsqrtf(fmaf(q[0], a.inv_d, a.eps));
 }
 
 // The same for two rows of values at once, with half as many reductions.
 template <bool VEC, int R, int NV>
-__device__ __forceinline__ void centre2(float (&v)[NV][kCols], float (&w)[NV][kCols], const NormArgs& a,
-                                        int l, float* buf, int& phase, float& rv, float& rw) {
+__device__ __forceinline__ void centre2(uint64_t (&v)[NV][kPairs], uint64_t (&w)[NV][kPairs],
+                                        const NormArgs& a, int l, float* buf, int& phase, float& rv,
+                                        float& rw) {
   if (a.layer) {
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < kCols; ++e) s[0] += v[j][e], s[1] += w[j][e];
+    float s[2] = {total(v), total(w)};
     row_sum<R, 2>(s, buf, phase);
     subtract<VEC, R, NV>(v, s[0] * a.inv_d, a, l);
     subtract<VEC, R, NV>(w, s[1] * a.inv_d, a, l);
   }
-  float q[2] = {0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < kCols; ++e) {
-      q[0] = fmaf(v[j][e], v[j][e], q[0]);
-      q[1] = fmaf(w[j][e], w[j][e], q[1]);
-    }
+  float q[2] = {total_squares(v), total_squares(w)};
   row_sum<R, 2>(q, buf, phase);
   rv = rsqrtf(fmaf(q[0], a.inv_d, a.eps));
   rw = rsqrtf(fmaf(q[1], a.inv_d, a.eps));
@@ -323,7 +363,7 @@ __global__ void __launch_bounds__(norm_threads<R>())
   const int l = R > 32 ? threadIdx.x : threadIdx.x % R;
   const int grp = R > 32 ? 0 : threadIdx.x / R;
   int phase = 0;
-  float g1[NV][kCols], b1[NV][kCols], rs[NV][kCols], g2[NV][kCols], b2[NV][kCols];
+  uint64_t g1[NV][kPairs], b1[NV][kPairs], rs[NV][kPairs], g2[NV][kPairs], b2[NV][kPairs];
   load_params<VEC, NV>(a.g1, 1.f, l, R, a.d, g1);
   load_params<VEC, NV>(a.b1, 0.f, l, R, a.d, b1);
   load_params<VEC, NV>(a.rs, 1.f, l, R, a.d, rs);
@@ -351,7 +391,7 @@ __global__ void __launch_bounds__(norm_threads<R>())
   // store nothing.
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < a.rows; row0 += step, row += step) {
     const bool live = row < a.rows;
-    float x[NV][kCols], y[NV][kCols], z[NV][kCols];
+    uint64_t x[NV][kPairs], y[NV][kPairs], z[NV][kPairs];
     if (VEC) copy_wait<D - 1>();
     const uint32_t slot = mine + stage * (Pl::kSlots * T * 16);
     ox.take(live, slot, l, a.d, x);
@@ -360,30 +400,40 @@ __global__ void __launch_bounds__(norm_threads<R>())
     fetch(stage, row + D * step);
     stage = stage + 1 == D ? 0 : stage + 1;
     if (a.y != nullptr) {
-      const float ry = a.g1 != nullptr ? centre<VEC, R, NV>(y, a, l, buf, phase) : 1.f;
+      if (a.z != nullptr) gate_values(z, a.gate_kind);
+      if (a.g1 != nullptr) {
+        const uint64_t ry = both(centre<VEC, R, NV>(y, a, l, buf, phase));
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) y[j][e] = f2_fma(f2_mul(y[j][e], ry), g1[j][e], b1[j][e]);
+      }
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) {
-          const float n = fmaf(y[j][e] * ry, g1[j][e], b1[j][e]);
-          const float act = a.z != nullptr ? gate_value(z[j][e], a.gate_kind) : 1.f;
-          x[j][e] = fmaf(rs[j][e] * act, n, x[j][e]);
-        }
+        for (int e = 0; e < kPairs; ++e)
+          x[j][e] = f2_fma(a.z != nullptr ? f2_mul(rs[j][e], z[j][e]) : rs[j][e], y[j][e], x[j][e]);
       if (a.o1 != nullptr && live) put_row<TR, R, NV, VEC>(a.o1, row, x, l, a.d);
     }
     if (a.o2 != nullptr) {
-      const float rr = centre<VEC, R, NV>(x, a, l, buf, phase);
+      const uint64_t rr = both(centre<VEC, R, NV>(x, a, l, buf, phase));
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) x[j][e] = fmaf(x[j][e] * rr, g2[j][e], b2[j][e]);
+        for (int e = 0; e < kPairs; ++e) x[j][e] = f2_fma(f2_mul(x[j][e], rr), g2[j][e], b2[j][e]);
       if (live) put_row<TB, R, NV, VEC>(a.o2, row, x, l, a.d);
     }
   }
 }
 
+// At 128 threads the backward takes the registers it wants (162, three blocks
+// per SM: 254 us over 400K x 128; cut to 128 for four blocks it spills and
+// takes 317); a block of 512 threads is alone on its SM.
+template <int R>
+__host__ __device__ constexpr int norm_blocks() { return R == 512 ? 1 : 0; }
+
 template <class TB, class TR, int R, int NV, bool VEC>
-__global__ void __launch_bounds__(norm_threads<R>())
+__global__ void __launch_bounds__(norm_threads<R>(), norm_blocks<R>())
     block_norm_backward_kernel(const NormArgs a) {
   using Pl = NormPlan<TB, TR, R, NV, VEC, true>;
   constexpr int T = Pl::T, G = Pl::G, D = Pl::D;
@@ -393,18 +443,18 @@ __global__ void __launch_bounds__(norm_threads<R>())
   const int l = R > 32 ? threadIdx.x : threadIdx.x % R;
   const int grp = R > 32 ? 0 : threadIdx.x / R;
   int phase = 0;
-  float g1[NV][kCols], b1[NV][kCols], rs[NV][kCols], g2[NV][kCols];
+  uint64_t g1[NV][kPairs], b1[NV][kPairs], rs[NV][kPairs], g2[NV][kPairs];
   load_params<VEC, NV>(a.g1, 1.f, l, R, a.d, g1);
   load_params<VEC, NV>(a.b1, 0.f, l, R, a.d, b1);
   load_params<VEC, NV>(a.rs, 1.f, l, R, a.d, rs);
   load_params<VEC, NV>(a.g2, 1.f, l, R, a.d, g2);
-  float acc[5][NV][kCols];  // dg1, db1, drs, dg2, db2
+  uint64_t acc[5][NV][kPairs];  // dg1, db1, drs, dg2, db2
 #pragma unroll
   for (int i = 0; i < 5; ++i)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) acc[i][j][e] = 0.f;
+      for (int e = 0; e < kPairs; ++e) acc[i][j][e] = 0ull;
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
   Operand<TR, R, NV, T, VEC> ox, odr;
   Operand<TB, R, NV, T, VEC> oy, oz, odu;
@@ -432,7 +482,7 @@ __global__ void __launch_bounds__(norm_threads<R>())
   // add nothing to the sums, and store nothing.
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < a.rows; row0 += step, row += step) {
     const bool live = row < a.rows;
-    float x[NV][kCols], dx[NV][kCols], y[NV][kCols], z[NV][kCols], h[NV][kCols];
+    uint64_t x[NV][kPairs], dx[NV][kPairs], y[NV][kPairs], z[NV][kPairs], h[NV][kPairs];
     if (VEC) copy_wait<D - 1>();
     const uint32_t slot = mine + stage * (Pl::kSlots * T * 16);
     ox.take(live && a.du != nullptr, slot, l, a.d, x);
@@ -450,58 +500,67 @@ __global__ void __launch_bounds__(norm_threads<R>())
     else if (a.g1 != nullptr)
       ry = centre<VEC, R, NV>(y, a, l, buf, phase);
     if (a.du != nullptr) {
-      float s[2] = {0.f, 0.f};
+      const uint64_t r2 = both(rr);
+      uint64_t s0 = 0ull, s1 = 0ull;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) {
-          const float xh = x[j][e] * rr, du = h[j][e];
-          acc[3][j][e] = fmaf(du, xh, acc[3][j][e]);
-          acc[4][j][e] += du;
+        for (int e = 0; e < kPairs; ++e) {
+          const uint64_t xh = f2_mul(x[j][e], r2), du = h[j][e];
+          acc[3][j][e] = f2_fma(du, xh, acc[3][j][e]);
+          acc[4][j][e] = f2_add(acc[4][j][e], du);
           x[j][e] = xh;
-          h[j][e] = du * g2[j][e];
-          s[0] = fmaf(h[j][e], xh, s[0]);
-          s[1] += h[j][e];
+          h[j][e] = f2_mul(du, g2[j][e]);
+          s0 = f2_fma(h[j][e], xh, s0);
+          s1 = f2_add(s1, h[j][e]);
         }
+      float s[2] = {f2_sum(s0), f2_sum(s1)};
       row_sum<R, 2>(s, buf, phase);
-      const float c1 = s[0] * a.inv_d, c2 = a.layer ? s[1] * a.inv_d : 0.f;
+      const uint64_t c1 = both(-s[0] * a.inv_d), c2 = both(a.layer ? -s[1] * a.inv_d : 0.f);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < kCols; ++e)
-          dx[j][e] = fmaf(rr, h[j][e] - c2 - x[j][e] * c1, dx[j][e]);
+        for (int e = 0; e < kPairs; ++e)
+          dx[j][e] = f2_fma(r2, f2_fma(x[j][e], c1, f2_add(h[j][e], c2)), dx[j][e]);
     }
     if (a.o1 != nullptr && live) put_row<TR, R, NV, VEC>(a.o1, row, dx, l, a.d);
     if (a.y == nullptr) continue;
-    float s[2] = {0.f, 0.f};
+    const uint64_t r1 = both(ry);
+    uint64_t s0 = 0ull, s1 = 0ull;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) {
-        const float yh = y[j][e] * ry;
-        const float n = fmaf(yh, g1[j][e], b1[j][e]);
-        float act = 1.f, slope = 0.f;
-        if (a.z != nullptr) slope = gate_slope(z[j][e], a.gate_kind, act);
-        const float ds = dx[j][e] * rs[j][e];
-        const float dn = ds * act;
-        z[j][e] = ds * n * slope;  // dz
-        acc[2][j][e] = fmaf(dx[j][e] * act, n, acc[2][j][e]);
-        acc[0][j][e] = fmaf(dn, yh, acc[0][j][e]);
-        acc[1][j][e] += dn;
-        const float p = dn * g1[j][e];
+      for (int e = 0; e < kPairs; ++e) {
+        const uint64_t yh = f2_mul(y[j][e], r1);
+        const uint64_t n = f2_fma(yh, g1[j][e], b1[j][e]);
+        const uint64_t ds = f2_mul(dx[j][e], rs[j][e]);
+        uint64_t dn = ds, n2 = n;  // n2: act n
+        if (a.z != nullptr) {
+          uint64_t act;
+          const uint64_t slope = gate_slope(z[j][e], a.gate_kind, act);
+          z[j][e] = f2_mul(f2_mul(ds, n), slope);  // dz
+          dn = f2_mul(ds, act);
+          n2 = f2_mul(act, n);
+        }
+        acc[2][j][e] = f2_fma(dx[j][e], n2, acc[2][j][e]);
+        acc[0][j][e] = f2_fma(dn, yh, acc[0][j][e]);
+        acc[1][j][e] = f2_add(acc[1][j][e], dn);
+        const uint64_t p = f2_mul(dn, g1[j][e]);
         y[j][e] = yh;
         dx[j][e] = p;
-        s[0] = fmaf(p, yh, s[0]);
-        s[1] += p;
+        s0 = f2_fma(p, yh, s0);
+        s1 = f2_add(s1, p);
       }
     if (a.o3 != nullptr && live) put_row<TB, R, NV, VEC>(a.o3, row, z, l, a.d);
     if (a.g1 != nullptr) {
+      float s[2] = {f2_sum(s0), f2_sum(s1)};
       row_sum<R, 2>(s, buf, phase);
-      const float c1 = s[0] * a.inv_d, c2 = a.layer ? s[1] * a.inv_d : 0.f;
+      const uint64_t c1 = both(-s[0] * a.inv_d), c2 = both(a.layer ? -s[1] * a.inv_d : 0.f);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) dx[j][e] = ry * (dx[j][e] - c2 - y[j][e] * c1);
+        for (int e = 0; e < kPairs; ++e)
+          dx[j][e] = f2_mul(r1, f2_fma(y[j][e], c1, f2_add(dx[j][e], c2)));
     }
     if (a.o2 != nullptr && live) put_row<TB, R, NV, VEC>(a.o2, row, dx, l, a.d);
   }
@@ -515,7 +574,12 @@ __global__ void __launch_bounds__(norm_threads<R>())
       if constexpr (G > 1) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) red[e * T + threadIdx.x] = acc[i][j][e];
+        for (int e = 0; e < kPairs; ++e) {
+          float lo, hi;
+          f2_unpack(acc[i][j][e], lo, hi);
+          red[2 * e * T + threadIdx.x] = lo;
+          red[(2 * e + 1) * T + threadIdx.x] = hi;
+        }
         __syncthreads();
         if (grp == 0) {
 #pragma unroll
@@ -530,7 +594,9 @@ __global__ void __launch_bounds__(norm_threads<R>())
 #pragma unroll
         for (int e = 0; e < kCols; ++e) {
           const int c = column<VEC>(l, j, e, R);
-          if (c < a.d) part[i * a.d + c] = acc[i][j][e];
+          float v[2];
+          f2_unpack(acc[i][j][e / 2], v[0], v[1]);
+          if (c < a.d) part[i * a.d + c] = v[e % 2];
         }
       }
     }
@@ -540,21 +606,24 @@ struct NormSums {
   float* out[5];
 };
 
-// out[i][c] = the blocks' column sums in ascending order (8 interleaved runs
+// out[i][c] = the blocks' column sums in ascending order (16 interleaved runs
 // per column in fp64, joined in a fixed order): bitwise reproducible.
-__global__ void __launch_bounds__(256) block_norm_sums_kernel(const float* part, int blocks, int d,
-                                                              NormSums o) {
-  __shared__ double red[8][32];
+constexpr int kRuns = 16;
+__global__ void __launch_bounds__(32 * kRuns) block_norm_sums_kernel(const float* part, int blocks, int d,
+                                                                     NormSums o) {
+  __shared__ double red[kRuns][32];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int e = blockIdx.x * 32 + lane, n = 5 * d;
   grid_dependency_wait();
   double s = 0.0;
-  if (e < n)
-    for (int b = run; b < blocks; b += 8) s += part[static_cast<int64_t>(b) * n + e];
+  if (e < n) {
+#pragma unroll 8
+    for (int b = run; b < blocks; b += kRuns) s += part[static_cast<int64_t>(b) * n + e];
+  }
   red[run][lane] = s;
   __syncthreads();
   if (run == 0 && e < n) {
-    for (int r = 1; r < 8; ++r) s += red[r][lane];
+    for (int r = 1; r < kRuns; ++r) s += red[r][lane];
     float* out = o.out[e / d];
     if (out != nullptr) out[e % d] = static_cast<float>(s);
   }
@@ -782,7 +851,7 @@ sa_status sa_block_norm_backward(const void* residual_out, int64_t ld_residual, 
   if (!a.sums) return SA_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((5 * d + 31) / 32);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * sa::kRuns);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -550,6 +550,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // range_begin (sa_internal.h) computed by a whole warp: every lane passes
 // the same arguments and gets the same row and user.  A 32-way search over
 // the users, one round of loads per factor of 32 in the batch size; for
