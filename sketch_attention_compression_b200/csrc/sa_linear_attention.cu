@@ -80,6 +80,33 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// ---------------------------------------------------------------- order of the users
+// Clears the header, checks the inputs and ranks the users by length, longest
+// first, so that a ragged batch does not end with its longest history on one
+// SM (48 users of up to 4099 rows at eight heads: 230 -> 197 us).  One block;
+// every user counts the longer ones.
+constexpr int kMostOrdered = 1024;
+
+__global__ void __launch_bounds__(kMostOrdered) order_kernel(const ScanCommon s, int32_t* order) {
+  __shared__ int64_t lens[kMostOrdered];
+  __shared__ uint32_t flags;
+  const int tid = threadIdx.x, n = static_cast<int>(s.batch);
+  if (tid < static_cast<int>(sizeof(WsHeader) / 4)) reinterpret_cast<uint32_t*>(s.header)[tid] = 0u;
+  int64_t mine = -1;
+  if (tid < n) {
+    int64_t lo, hi;
+    user_rows(s, tid, lo, hi);
+    mine = hi - lo;
+  }
+  lens[tid] = mine;
+  __syncthreads();
+  check_inputs(s, &flags);
+  if (tid >= n) return;
+  int rank = 0;
+  for (int i = 0; i < n; ++i) rank += lens[i] > mine || (lens[i] == mine && i < tid);
+  order[rank] = tid;
+}
+
 // ---------------------------------------------------------------- one step
 // S <- l S + k v^T, o = mul S^T q for one row of each listed state.  Bound
 // by reading and writing the state once: a thread takes four columns of
@@ -247,6 +274,8 @@ int64_t split_rows(const SplitRule& rule, int64_t batch, int64_t rows, int64_t m
   return whole > share + share / 2 + segment + rule.launches ? segment : 0;
 }
 
+constexpr size_t kOrderBytes = kMostOrdered * sizeof(int32_t);
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // The states between segments, one direction.
@@ -267,8 +296,9 @@ int device_sms() {
 }
 
 // Runs n scans (n = 1: the forward; n = 3: dq, dk, dv) of one batch.  The
-// workspace: header | states between segments, forward, reverse | a copy of
-// the initial states (forward scans whose final states replace them).
+// workspace: header | order of the users | states between segments, forward,
+// reverse | a copy of the initial states (forward scans whose final states
+// replace them).
 // `inputs` are q, k, v and, for the gradients, d_out.
 cudaError_t run_scans(ScanPass* passes, int n, const ScanInput* inputs, const ScanCommon& s,
                       int64_t max_rows, int d_k, int d_v, bool bf16, int sms, cudaStream_t st) {
@@ -281,7 +311,8 @@ cudaError_t run_scans(ScanPass* passes, int n, const ScanInput* inputs, const Sc
                               inputs[i].row, inputs[i].head, 128);
   const int64_t segment = split_rows(tc ? kSplitTc : kSplitSimt, s.batch, s.rows, max_rows, s.heads,
                                      n, sms);
-  uint8_t* ws = reinterpret_cast<uint8_t*>(s.header) + kWsHeaderBytes;
+  int32_t* order = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(s.header) + kWsHeaderBytes);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(order) + kOrderBytes;
   const size_t half = bound_bytes(s.rows, segment, s.heads, elems);
   for (int i = 0; i < n; ++i) passes[i].bound = reinterpret_cast<float*>(ws + passes[i].reverse * half);
   ScanArgs t = {};
@@ -295,7 +326,15 @@ cudaError_t run_scans(ScanPass* passes, int n, const ScanInput* inputs, const Sc
   cudaError_t err = cudaSuccess;
   if (tc && slots * s.heads * n > sms) {
     counter = reinterpret_cast<unsigned long long*>(s.header) + 8;
-    err = cudaMemsetAsync(s.header, 0, kWsHeaderBytes, st);
+    const int64_t longest = max_rows > 0 && max_rows < s.rows ? max_rows : s.rows;
+    if (segment == 0 && s.batch <= kMostOrdered && s.batch * longest > s.rows + s.rows / 8) {
+      order_kernel<<<1, kMostOrdered, 0, st>>>(s, order);
+      err = cudaGetLastError();
+      t.order = order;
+      t.check = 0;
+    } else {
+      err = cudaMemsetAsync(s.header, 0, kWsHeaderBytes, st);
+    }
   }
   auto launch = [&](ScanArgs& u, bool states_only) {
     u.items = slots * s.heads * u.passes;
@@ -370,7 +409,7 @@ size_t sa_workspace_bytes_linear_attention(int heads, int d_k, int d_v, int64_t 
                                   : 2 * sa::bound_bytes(total_rows, seg, heads, elems);
     if (n > most) most = n;
   }
-  return sa::kWsHeaderBytes + most;
+  return sa::kWsHeaderBytes + sa::kOrderBytes + most;
 }
 
 sa_status sa_linear_attention_forward(const void* q, int64_t q_row, int64_t q_head, const void* k,

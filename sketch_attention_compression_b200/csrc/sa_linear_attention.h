@@ -79,6 +79,7 @@ struct ScanArgs {
   int64_t segment;         // rows per segment (> rows where nothing is split)
   int64_t items;           // segment slots * heads * passes
   unsigned long long* counter;  // next item (tensor-core scan), or null: every grid-th item
+  const int32_t* order;    // users by length, longest first, or null: as they come (whole histories)
 };
 
 // One scan of one segment of a user's rows for one head.
@@ -124,7 +125,8 @@ __device__ __forceinline__ bool item_of(const ScanArgs& t, int64_t x, int lane, 
   int64_t b = 0, base = slot;
   if (whole) {
     b = slot < t.s.batch ? slot : t.s.batch - 1;
-    base = b;
+    if (t.order != nullptr) b = t.order[b];
+    base = slot;
   } else {
     // Largest b with slot_base(b) <= slot: a 32-way search.
     int64_t hi = t.s.batch - 1;
@@ -152,7 +154,7 @@ __device__ __forceinline__ bool item_of(const ScanArgs& t, int64_t x, int lane, 
   it.pass = pass;
   it.first = rev ? i == count - 1 : i == 0;
   it.last = rev ? i == 0 : i == count - 1;
-  const int64_t bound = base - b;
+  const int64_t bound = base - b;  // (unused where nothing is split)
   it.from = it.first ? -1 : (bound + (rev ? i : i - 1)) * t.s.heads + head;
   it.to = it.last ? -1 : (bound + (rev ? i - 1 : i)) * t.s.heads + head;
   return !states_only || !it.last;

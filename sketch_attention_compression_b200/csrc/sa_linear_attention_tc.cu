@@ -217,11 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_ready = bars + 15;           // P~ stored
   uint64_t* b_ready = bars + 16;           // w b stored
   uint64_t* o_full = bars + 17;            // M3 done (and M2)
-  uint64_t* d_full = bars + 18;            // M4 done
-  uint64_t* o_read = bars + 19;            // warps 12-15 have read O1, O2
-  uint64_t* tab_ready = bars + 20;         // [2] a table of powers stored (state, weight warps)
-  uint64_t* drain = bars + 22;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
+  uint64_t* d_full = bars + 18;            // [2] M4 done (chunks in turn)
+  uint64_t* o_read = bars + 20;            // warps 12-15 have read O1, O2
+  uint64_t* tab_ready = bars + 21;         // [2] a table of powers stored (state, weight warps)
+  uint64_t* drain = bars + 23;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(b_ready, 8);
     mbar_init(o_full, 1);
     mbar_init(d_full, 1);
+    mbar_init(d_full + 1, 1);
     mbar_init(o_read, 4);
     mbar_init(tab_ready, 8);
     mbar_init(tab_ready + 1, 4);
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the next barrier in turns with its instructions.  Products are issued
     // in groups of four steps of K (64 columns of a K-major operand, 64 rows
     // of an MN-major one).
+    auto d_col = [&](uint32_t c) { return tmem + (STATE ? (c & 1u) * 256u : Pl::kColD); };
     auto group = [&](uint32_t acc, uint64_t da, int step_a, uint64_t db, int step_b, uint32_t id,
                      bool first) {
 #pragma unroll
@@ -365,6 +367,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = sbase + st * Pl::kStage;
         const uint64_t cm = smem_desc(d + Pl::kC, kBox, 1024, 2);  // c, MN-major
         bool next = false;
+        auto ahead_m1 = [&]() {
+          if (c + 1 >= chunks) return;
+          next = __all_sync(0xFFFFFFFFu,
+                            mbar_test_wait(full + (n + 1) % kStages, ((n + 1) / kStages) & 1u));
+          if (!next) return;
+          tc_fence_after();
+          if (lane == 0) m1(n + 1);
+          __syncwarp();
+        };
         if (!STATE) {
           if (!ahead) {
             if (!warp_wait(full + st, (n / kStages) & 1u, abort_flag, sticky)) { ok = false; break; }
@@ -400,16 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(o_full);
           }
           __syncwarp();
-          // The next chunk's M1 goes before this chunk's M4 if its tiles are there.
-          if (c + 1 < chunks) {
-            next = __all_sync(0xFFFFFFFFu,
-                              mbar_test_wait(full + (n + 1) % kStages, ((n + 1) / kStages) & 1u));
-            if (next) {
-              tc_fence_after();
-              if (lane == 0) m1(n + 1);
-              __syncwarp();
-            }
-          }
+          // The next chunk's M1 goes before this chunk's M4 where s3 waits for
+          // it, if its tiles are there.
+          if (Pl::kOwn) ahead_m1();
         }
         if (!warp_wait(b_ready, ph, abort_flag, sticky)) { ok = false; break; }
         tc_fence_after();
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto product = [&](uint64_t part, uint32_t id, bool first) {
 #pragma unroll
             for (int g = 0; g < 2; ++g)
-              group(tmem + Pl::kColD, cm + g * 4 * kStepMn, kStepMn, part + g * 4 * kStepMn, kStepMn, id,
+              group(d_col(n), cm + g * 4 * kStepMn, kStepMn, part + g * 4 * kStepMn, kStepMn, id,
                     first && g == 0);
           };
           if (Pl::kOwn) {
@@ -434,9 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (three) product(smem_desc(sbase + Pl::kS, kBox, 1024, 2), id_128, false);
           }
           mma_commit(empty + st);
-          mma_commit(d_full);
+          mma_commit(d_full + st);
         }
         __syncwarp();
+        if (!STATE && !Pl::kOwn) ahead_m1();
         ahead = next;
       }
     }
@@ -456,27 +461,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t S[HA / 2];  // pairs of rows of the state
     ScanItem it;
     auto power = [&](int e) { return ld_shared_f32(tab + e * 4); };
-    // S <- (f + fl) S + D, once M4 of the chunk before is done.
-    auto add_d = [&](float f, float fl, bool three) {
-      if (!ok || !warp_wait(d_full, (n - 1) & 1u, abort_flag, sticky)) {
+    // S <- (f + fl) S + D of chunk `of`, once its M4 is done.
+    auto add_d = [&](uint32_t of, float f, float fl, bool three) {
+      if (!ok || !warp_wait(d_full + (of & 1u), (of >> 1) & 1u, abort_flag, sticky)) {
         ok = false;
         return;
       }
       tc_fence_after();
       if (state_row) {
         const uint64_t f2 = f2_pack(f, f), fl2 = f2_pack(fl, fl);
+        const uint32_t d = lane_base + (STATE ? (of & 1u) * 256u : Pl::kColD) + hf * HA;
 #pragma unroll
         for (int j = 0; j < HA / 16; ++j) {
           uint32_t v[16], lo[16];
-          tmem_ld16(lane_base + Pl::kColD + hf * HA + j * 16, v);
-          if (Pl::kOwn) tmem_ld16(lane_base + Pl::kColD + 64 + hf * HA + j * 16, lo);
+          tmem_ld16(d + j * 16, v);
+          if (Pl::kOwn) tmem_ld16(d + 64 + j * 16, lo);
           tmem_wait_ld();
           tmem_pin16(v);
           if (Pl::kOwn) {
             tmem_pin16(lo);
             if (DC == 64 && three) {
               uint32_t low[16];
-              tmem_ld16(lane_base + Pl::kColD + 128 + hf * HA + j * 16, low);
+              tmem_ld16(d + 128 + j * 16, low);
               tmem_wait_ld();
               tmem_pin16(low);
 #pragma unroll
@@ -588,8 +594,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!STATE && !warp_wait(p_full, ph, abort_flag, sticky)) { ok = false; break; }
           split();
         }
+        if (STATE && early) {
+          // Two places for D: the chunk before is added while M4 runs.
+          fence_proxy_async_smem();
+          warp_arrive(b_ready, lane);
+        }
         // s1
-        if (c > 0) add_d(f, fl, p.parts == 3);
+        if (c > 0) add_d(n - 1, f, fl, p.parts == 3);
         if (!ok) break;
         f = power(L - skip);
         fl = L - skip == 128 ? power(129) : 0.f;
@@ -617,8 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!STATE && !warp_wait(a_free, ph, abort_flag, sticky)) { ok = false; break; }
           split();
         }
-        fence_proxy_async_smem();
-        warp_arrive(b_ready, lane);
+        if (!STATE || !early) {
+          fence_proxy_async_smem();
+          warp_arrive(b_ready, lane);
+        }
         // s4
         if (!STATE) {
           if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
@@ -630,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (chunks > 0) add_d(f, fl, p.parts == 3);
+      if (chunks > 0) add_d(n - 1, f, fl, p.parts == 3);
       if (!ok) break;
       // The state behind the last row.
       float* dst = nullptr;
