@@ -20,9 +20,9 @@
 // two stages), warp 1 issues the MMAs.  Warps 4-11 hold the state, two warps
 // per TMEM lane quarter, each with half of the columns; per chunk they
 //   s1  add D of the chunk before to S and store S~
-//   s3  split w b: the first part over b, which M1 has read, the others in
-//       places of their own (da = 64), or over a and in S~'s place once M2
-//       has read those
+//   s3  split w b: into places of their own a chunk ahead (da = dc = 64),
+//       the first part over b once M1 has read it (da = 64), or also the
+//       others over a and in S~'s place once M2 has read those
 //   s4  store most columns of out, while M4 runs
 // and warps 12-15, one row of the chunk per thread,
 //   s2  turn P into P~ (TMEM to TMEM), while M2 and s3 run
@@ -59,10 +59,12 @@ template <int DA, int DC>
 struct TcPlan {
   static constexpr int kA = 0;                          // within a stage
   static constexpr int kB = kA + (DA / 64) * kBox;
-  // The low parts of w b.  da = 64: boxes of their own behind b; else they
-  // lie over a and in S~'s place.
-  static constexpr bool kOwn = DA == 64;
-  static constexpr int kC = kB + (kOwn ? 3 : DA / 64) * kBox;
+  // The parts of w b.  da = dc = 64: boxes of their own behind b; da = 64:
+  // the first one over b, the others behind it; else over b, over a and in
+  // S~'s place.
+  static constexpr bool kOwn = DA == 64, kApart = DA == 64 && DC == 64;
+  static constexpr int kHi = kApart ? kB + kBox : kB;
+  static constexpr int kC = kOwn ? kHi + 3 * kBox : kB + (DA / 64) * kBox;
   static constexpr int kStage = kC + (DC / 64) * kBox;
   static constexpr int kS = kStages * kStage;           // S~^T: da / 64 boxes of dc rows
   static constexpr int kSBox = DC * 128;
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           // c^T times the parts of w b, both MN-major.
           const bool three = t.p[it.pass].parts == 3;
-          const uint64_t hi = smem_desc(d + Pl::kB, kBox, 1024, 2);
+          const uint64_t hi = smem_desc(d + Pl::kHi, kBox, 1024, 2);
           auto product = [&](uint64_t part, uint32_t id, bool first) {
 #pragma unroll
             for (int g = 0; g < 2; ++g)
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // One product for the parts side by side, 64 columns of D each;
             // with dc = 128 TMEM has room for two of them.
             product(hi, DC == 64 && three ? id_192 : id_128, true);
-            if (DC == 128 && three) product(smem_desc(d + Pl::kB + 2 * kBox, kBox, 1024, 2), id_64, false);
+            if (DC == 128 && three) product(smem_desc(d + Pl::kHi + 2 * kBox, kBox, 1024, 2), id_64, false);
           } else {
             product(hi, id_128, true);
             product(smem_desc(d + Pl::kA, kBox, 1024, 2), id_128, false);
@@ -531,57 +533,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       float f = 0.f, fl = 0.f;  // decay of S over the chunk before
       // s3 is early where its places do not depend on M2.
       const bool early = Pl::kOwn || (STATE && p.parts == 2);
-      for (int64_t c = 0; c < chunks; ++c, ++n) {
-        const uint32_t st = n % kStages, ph = n & 1u;
-        const uint32_t d = sbase + st * Pl::kStage;
-        const int64_t r0 = it.lo + 128 * (rev ? chunks - 1 - c : c);
-        const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
-        // A reverse scan's first chunk of a user takes the start state undecayed.
-        const int skip = rev && it.first && c == 0 ? 1 : 0;
-        // s3: w b in two or three bf16 parts, the first one over b.
-        auto split = [&]() {
-          constexpr int kRowStep = kStateThreads / (DA / 8);  // a multiple of 8
-          const int u = ctid % (DA / 8), first = ctid / (DA / 8);
-          const uint32_t o = (u >> 3) * kBox + swz(first, u & 7);
-          uint32_t src = d + Pl::kB + o;
-          uint32_t dst = Pl::kOwn ? src + kBox : d + Pl::kA + o;
-          uint32_t third = Pl::kOwn ? src + 2 * kBox : sbase + Pl::kS + o;
-          const bool three = p.parts == 3;
-          const uint64_t minus = f2_pack(-1.f, -1.f);
+      // With places apart it is done a chunk ahead, while M2 and M3 run.
+      constexpr bool kAhead = !STATE && Pl::kApart;
+      // s3: w b in two or three bf16 parts, for a chunk of L rows at d.
+      auto split = [&](uint32_t d, int L) {
+        constexpr int kRowStep = kStateThreads / (DA / 8);  // a multiple of 8
+        const int u = ctid % (DA / 8), first = ctid / (DA / 8);
+        const uint32_t o = (u >> 3) * kBox + swz(first, u & 7);
+        uint32_t src = d + Pl::kB + o;
+        uint32_t hi_dst = d + Pl::kHi + o;
+        uint32_t dst = Pl::kOwn ? hi_dst + kBox : d + Pl::kA + o;
+        uint32_t third = Pl::kOwn ? hi_dst + 2 * kBox : sbase + Pl::kS + o;
+        const bool three = p.parts == 3;
+        const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll 2
-          for (int r = first; r < 128; r += kRowStep) {
-            const float w1 = r < L ? power(rev ? r : L - 1 - r) : 0.f;
-            const uint64_t w = f2_pack(w1, w1);
-            const uint4 x = ld_shared_v4u(src);
-            uint32_t v[4] = {x.x, x.y, x.z, x.w};
-            if (r >= L) v[0] = v[1] = v[2] = v[3] = 0u;
-            uint64_t y[4];
-            uint32_t hi[4], lo[4];
+        for (int r = first; r < 128; r += kRowStep) {
+          const float w1 = r < L ? power(rev ? r : L - 1 - r) : 0.f;
+          const uint64_t w = f2_pack(w1, w1);
+          const uint4 x = ld_shared_v4u(src);
+          uint32_t v[4] = {x.x, x.y, x.z, x.w};
+          if (r >= L) v[0] = v[1] = v[2] = v[3] = 0u;
+          uint64_t y[4];
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = f2_mul(w, f2_pack(bf_lo(v[i]), bf_hi(v[i])));
+            float y0, y1;
+            f2_unpack(y[i], y0, y1);
+            hi[i] = pack_bf16x2(y0, y1);
+            y[i] = f2_fma(minus, f2_pack(bf_lo(hi[i]), bf_hi(hi[i])), y[i]);
+            f2_unpack(y[i], y0, y1);
+            lo[i] = pack_bf16x2(y0, y1);
+          }
+          st_shared_v4(hi_dst, hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(dst, lo[0], lo[1], lo[2], lo[3]);
+          if (three) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              y[i] = f2_mul(w, f2_pack(bf_lo(v[i]), bf_hi(v[i])));
               float y0, y1;
-              f2_unpack(y[i], y0, y1);
+              f2_unpack(f2_fma(minus, f2_pack(bf_lo(lo[i]), bf_hi(lo[i])), y[i]), y0, y1);
               hi[i] = pack_bf16x2(y0, y1);
-              y[i] = f2_fma(minus, f2_pack(bf_lo(hi[i]), bf_hi(hi[i])), y[i]);
-              f2_unpack(y[i], y0, y1);
-              lo[i] = pack_bf16x2(y0, y1);
             }
-            st_shared_v4(src, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(dst, lo[0], lo[1], lo[2], lo[3]);
-            if (three) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float y0, y1;
-                f2_unpack(f2_fma(minus, f2_pack(bf_lo(lo[i]), bf_hi(lo[i])), y[i]), y0, y1);
-                hi[i] = pack_bf16x2(y0, y1);
-              }
-              st_shared_v4(third, hi[0], hi[1], hi[2], hi[3]);
-            }
-            src += kRowStep * 128, dst += kRowStep * 128, third += kRowStep * 128;
+            st_shared_v4(third, hi[0], hi[1], hi[2], hi[3]);
           }
-        };
-        if (!warp_wait(full + st, (n / kStages) & 1u, abort_flag, sticky)) { ok = false; break; }
+          src += kRowStep * 128, hi_dst += kRowStep * 128, dst += kRowStep * 128, third += kRowStep * 128;
+        }
+      };
+      // Waits for the tiles of chunk c, number m; s3 too where its places do
+      // not depend on M2.
+      auto tiles = [&](int64_t c, uint32_t m) {
+        const uint32_t d = sbase + (m % kStages) * Pl::kStage;
+        const int64_t r0 = it.lo + 128 * (rev ? chunks - 1 - c : c);
+        const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
+        if (!warp_wait(full + m % kStages, (m / kStages) & 1u, abort_flag, sticky)) return false;
         if (L < 128) {
           // Rows behind the end belong to another user or to nobody: c's must
           // not reach the sums, whatever they hold.
@@ -591,9 +595,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (early) {
-          if (!STATE && !warp_wait(p_full, ph, abort_flag, sticky)) { ok = false; break; }
-          split();
+          if (!STATE && !Pl::kApart && !warp_wait(p_full, m & 1u, abort_flag, sticky)) return false;
+          split(d, L);
         }
+        return true;
+      };
+      for (int64_t c = 0; c < chunks; ++c, ++n) {
+        const uint32_t st = n % kStages, ph = n & 1u;
+        const uint32_t d = sbase + st * Pl::kStage;
+        const int64_t r0 = it.lo + 128 * (rev ? chunks - 1 - c : c);
+        const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
+        // A reverse scan's first chunk of a user takes the start state undecayed.
+        const int skip = rev && it.first && c == 0 ? 1 : 0;
+        if ((!kAhead || c == 0) && !tiles(c, n)) { ok = false; break; }
         if (STATE && early) {
           // Two places for D: the chunk before is added while M4 runs.
           fence_proxy_async_smem();
@@ -626,12 +640,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!early) {
           if (!STATE && !warp_wait(a_free, ph, abort_flag, sticky)) { ok = false; break; }
-          split();
+          split(d, L);
         }
         if (!STATE || !early) {
           fence_proxy_async_smem();
           warp_arrive(b_ready, lane);
         }
+        if (kAhead && c + 1 < chunks && !tiles(c + 1, n + 1)) { ok = false; break; }
         // s4
         if (!STATE) {
           if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
