@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(256)
   const float whole = static_cast<float>(exp(g * static_cast<double>(segment)));
   const int64_t tail = n - (count - 1) * segment - 1;  // the last segment's rows but one
   const float first = a.reverse ? static_cast<float>(exp(g * static_cast<double>(tail))) : whole;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 16;
   float4 x[kAhead];
   auto at = [&](int64_t j) {
     return reinterpret_cast<float4*>(p + (a.reverse ? count - 2 - j : j) * step);
@@ -255,17 +255,24 @@ sa_status on_sm100() {
 // rows or the longest history (equal histories in rounds, unequal ones end
 // with the longest), whichever is more; split, the share, the states' sums
 // (about half as much again), one segment and the extra launches.  Four
-// segments per SM even out the segments' ends.
+// segments per SM even out the segments' ends where the share is long; a
+// short share is one segment, so that there are no more of them than SMs.
 struct SplitRule {
-  int64_t tile, least, launches;  // rows: chunk, shortest segment, the extra launches' worth
+  int64_t tile, least, even, launches;  // rows: chunk, shortest segment, shortest of four per
+                                        // SM, the extra launches' worth
 };
-constexpr SplitRule kSplitSimt = {64, 64, 32}, kSplitTc = {128, 512, 1024};
+// Tensor cores, us: 1 history x 1500 rows, 4 heads of 128: 29 split, 55
+// whole; 1 x 20000, 2 heads of 64: 34 in segments of the share, 45 in shorter
+// ones.
+constexpr SplitRule kSplitSimt = {64, 64, 64, 32}, kSplitTc = {128, 256, 1024, 384};
 
 int64_t split_rows(const SplitRule& rule, int64_t batch, int64_t rows, int64_t max_rows, int heads,
                    int scans, int sms) {
   const int64_t longest = max_rows > 0 && max_rows < rows ? max_rows : rows;
   const int64_t share = rows * heads * scans / sms;
-  int64_t segment = (share / 4 + rule.tile - 1) / rule.tile * rule.tile;
+  auto tiles = [&](int64_t x) { return (x + rule.tile - 1) / rule.tile * rule.tile; };
+  int64_t segment = tiles(share / 4);
+  if (segment < rule.even) segment = tiles(share) < rule.even ? tiles(share) : rule.even;
   if (segment < rule.least) segment = rule.least;
   if (longest < 2 * segment) return 0;
   const int64_t waves = (batch * heads * scans + sms - 1) / sms;
