@@ -132,6 +132,17 @@ def test_integers_are_exact(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("users,heads", [(300, 2), (1100, 1)])
+def test_more_items_than_sms(users, heads, dtype):
+    """Ragged batches of more users than SMs, empty ones among them, also of
+    more than are ordered by length."""
+    lens = [(i * 37) % 23 for i in range(users)]
+    lens[users // 2] = 260
+    x, w = _make(lens, heads, 64, 64, dtype, seed=users)
+    _check(x, w, dtype, 0.125, max_rows=260)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_a_split_history_continues_from_its_state(dtype):
     """Two calls, the second from the first one's states, in place."""
     import torch
