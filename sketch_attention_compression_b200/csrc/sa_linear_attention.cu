@@ -343,11 +343,11 @@ cudaError_t run_scans(ScanPass* passes, int n, const ScanInput* inputs, const Sc
       err = cudaMemsetAsync(s.header, 0, kWsHeaderBytes, st);
     }
   }
-  auto launch = [&](ScanArgs& u, bool states_only) {
+  auto launch = [&](ScanArgs& u, bool states_only, bool beside) {
     u.items = slots * s.heads * u.passes;
     if (!tc) return launch_scan_simt(u, bf16, states_only, st);
     if (counter != nullptr) u.counter = counter++;
-    return launch_scan_tc(u, maps, states_only, sms, st);
+    return launch_scan_tc(u, maps, states_only, beside, sms, st);
   };
   if (segment != 0) {
     if (n == 1 && passes[0].ends != nullptr && passes[0].ends == passes[0].fin) {
@@ -373,7 +373,7 @@ cudaError_t run_scans(ScanPass* passes, int n, const ScanInput* inputs, const Sc
       o.da = d_k, o.dc = d_v;
       chain[p.reverse] = {p.reverse, p.ends, p.ends_mul, p.bound};
     }
-    if (err == cudaSuccess) err = launch(u, true);
+    if (err == cudaSuccess) err = launch(u, true, false);
     t.check = 0;
     if (err == cudaSuccess) {
       const dim3 grid(static_cast<unsigned>(s.batch * s.heads),
@@ -382,12 +382,13 @@ cudaError_t run_scans(ScanPass* passes, int n, const ScanInput* inputs, const Sc
       err = cudaGetLastError();
     }
   }
-  // Scans of one shape share a launch.
+  // Scans of one shape share a launch; those of the other shape run beside it.
   for (int i = 0; i < n && err == cudaSuccess;) {
     ScanArgs u = t;
     const int da = passes[i].da, dc = passes[i].dc;
+    const bool beside = i > 0;
     for (; i < n && passes[i].da == da && passes[i].dc == dc; ++i) u.p[u.passes++] = passes[i];
-    err = launch(u, false);
+    err = launch(u, false, beside);
     t.check = 0;
   }
   return err;

@@ -38,6 +38,8 @@
 // starts each segment from its own.
 #pragma once
 
+#include <atomic>
+
 #include "sa_internal.h"
 
 namespace sa {
@@ -182,17 +184,32 @@ __device__ __forceinline__ void check_inputs(const ScanCommon& s, uint32_t* shar
   }
 }
 
+// Lets `kernel` use `bytes` of shared memory on the current device; asked of
+// the runtime once per device (`done`: a bit per device).
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
 // Launches one scan (or, with states_only, the sums of its segments' states,
 // written to p[].bound) on the CUDA cores (sa_linear_attention_simt.cu).
 cudaError_t launch_scan_simt(const ScanArgs& t, bool bf16, bool states_only, cudaStream_t st);
 
 // The same on the tensor cores (sa_linear_attention_tc.cu), bf16 inputs whose
-// tensor maps the passes name.
+// tensor maps the passes name.  `beside`: the launch reads nothing that the
+// one before it writes and may run beside it.
 struct ScanMaps {
   CUtensorMap m[4];
 };
-cudaError_t launch_scan_tc(const ScanArgs& t, const ScanMaps& maps, bool states_only, int sms,
-                           cudaStream_t st);
+cudaError_t launch_scan_tc(const ScanArgs& t, const ScanMaps& maps, bool states_only, bool beside,
+                           int sms, cudaStream_t st);
 bool scan_tc_usable(const ScanInput& in);  // addresses and strides that TMA takes
 
 }  // namespace sa

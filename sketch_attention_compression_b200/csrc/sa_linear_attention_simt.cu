@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_simt_kernel(const __grid_con
 template <class T, int DA, int DC, bool STATE>
 cudaError_t launch(const ScanArgs& t, cudaStream_t st) {
   constexpr int smem = SimtPlan<DA, DC>::kSmem;
-  const cudaError_t err = cudaFuncSetAttribute(
-      scan_simt_kernel<T, DA, DC, STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t err = allow_smem(scan_simt_kernel<T, DA, DC, STATE>, smem, allowed);
   if (err != cudaSuccess) return err;
   const int64_t most = int64_t{1} << 30;
   scan_simt_kernel<T, DA, DC, STATE>

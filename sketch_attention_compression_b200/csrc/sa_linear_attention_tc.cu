@@ -206,6 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
+  // The scans of one call's other shape may start beside this launch; this
+  // one ends after the launch that it was started beside.
+  grid_dependency_launch();
   if (t.check && blockIdx.x == 0) check_inputs(t.s, reinterpret_cast<uint32_t*>(smem));
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Pl::kBars);
@@ -776,24 +779,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  grid_dependency_wait();
 }
 
 template <int DA, int DC, bool STATE>
-cudaError_t launch(const ScanMaps& m, const ScanArgs& t, int sms, cudaStream_t st) {
+cudaError_t launch(const ScanMaps& m, const ScanArgs& t, bool beside, int sms, cudaStream_t st) {
   using Pl = TcPlan<DA, DC>;
-  cudaError_t err = cudaFuncSetAttribute(scan_tc_kernel<DA, DC, STATE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t err = allow_smem(scan_tc_kernel<DA, DC, STATE>, Pl::kSmem, allowed);
   if (err != cudaSuccess) return err;
-  const int64_t grid = t.items < sms ? t.items : sms;
-  scan_tc_kernel<DA, DC, STATE><<<static_cast<unsigned>(grid), kThreads, Pl::kSmem, st>>>(m, t);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(t.items < sms ? t.items : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Pl::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, scan_tc_kernel<DA, DC, STATE>, m, t);
 }
 
 template <bool STATE>
-cudaError_t launch_any(int da, int dc, const ScanMaps& m, const ScanArgs& t, int sms, cudaStream_t st) {
-  if (da == 64)
-    return dc == 64 ? launch<64, 64, STATE>(m, t, sms, st) : launch<64, 128, STATE>(m, t, sms, st);
-  return dc == 64 ? launch<128, 64, STATE>(m, t, sms, st) : launch<128, 128, STATE>(m, t, sms, st);
+cudaError_t launch_any(const ScanMaps& m, const ScanArgs& t, bool beside, int sms, cudaStream_t st) {
+  if (t.p[0].da == 64)
+    return t.p[0].dc == 64 ? launch<64, 64, STATE>(m, t, beside, sms, st)
+                           : launch<64, 128, STATE>(m, t, beside, sms, st);
+  return t.p[0].dc == 64 ? launch<128, 64, STATE>(m, t, beside, sms, st)
+                         : launch<128, 128, STATE>(m, t, beside, sms, st);
 }
 
 }  // namespace
@@ -803,11 +817,10 @@ bool scan_tc_usable(const ScanInput& in) {
          in.head > 0 && in.head % 8 == 0;
 }
 
-cudaError_t launch_scan_tc(const ScanArgs& t, const ScanMaps& maps, bool states_only, int sms,
-                           cudaStream_t st) {
-  const int da = t.p[0].da, dc = t.p[0].dc;
-  return states_only ? launch_any<true>(da, dc, maps, t, sms, st)
-                     : launch_any<false>(da, dc, maps, t, sms, st);
+cudaError_t launch_scan_tc(const ScanArgs& t, const ScanMaps& maps, bool states_only, bool beside,
+                           int sms, cudaStream_t st) {
+  return states_only ? launch_any<true>(maps, t, beside, sms, st)
+                     : launch_any<false>(maps, t, beside, sms, st);
 }
 
 }  // namespace sa
