@@ -797,6 +797,14 @@ def _buffer(t, name, device):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _dense_like(t):
+    """A dense tensor of t's shape and type (empty_like is the quickest
+    allocation, but keeps other strides)."""
+    torch = _torch()
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype,
+                                                                     device=t.device)
+
+
 def _attention_shapes(q, v, offsets):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be (rows, heads, d)")
@@ -827,7 +835,7 @@ def linear_attention_forward(q, k, v, log_decay, offsets, scale, initial_state=N
             *_strided(v, "v", (N, H, dv), dtype, device))
     bound = 0 if max_rows is None else int(max_rows)
     if out is None:
-        out = torch.empty((N, H, dv), dtype=dtype, device=q.device)
+        out = _dense_like(v)
     if final_state is None:
         final_state = torch.empty(states, dtype=f32, device=q.device)
     if workspace is None:
@@ -858,12 +866,10 @@ def linear_attention_backward(q, k, v, log_decay, offsets, scale, d_out, initial
             *_strided(v, "v", (N, H, dv), dtype, device))
     grad = _strided(d_out, "d_out", (N, H, dv), dtype, device)
     bound = 0 if max_rows is None else int(max_rows)
-    out = dict(dq=torch.empty((N, H, dk), dtype=dtype, device=q.device),
-               dk=torch.empty((N, H, dk), dtype=dtype, device=q.device),
-               dv=torch.empty((N, H, dv), dtype=dtype, device=q.device))
+    out = dict(dq=_dense_like(q), dk=_dense_like(k), dv=_dense_like(v))
     ds0 = None
     if initial_state is not None:
-        ds0 = out["d_initial_state"] = torch.empty(states, dtype=f32, device=q.device)
+        ds0 = out["d_initial_state"] = _dense_like(initial_state)
     if workspace is None:
         workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
                                 dtype=torch.uint8, device=q.device)
@@ -894,7 +900,7 @@ def linear_attention_step(state, q, k, v, log_decay, scale, slots=None, out=None
     args = (*_strided(q, "q", (B, H, dk), dtype, device), *_strided(k, "k", (B, H, dk), dtype, device),
             *_strided(v, "v", (B, H, dv), dtype, device))
     if out is None:
-        out = torch.empty((B, H, dv), dtype=dtype, device=q.device)
+        out = _dense_like(v)
     _check(lib.sa_linear_attention_step(
         *args, _vector(log_decay, "log_decay", (H,), f32, device),
         _vector(slots, "slots", (B,), torch.int64, device), B, S, H, dk, dv, _dtype_code(dtype), float(scale),
@@ -957,9 +963,10 @@ def block_norm_forward(residual, block=None, gate=None, post_gain=None, post_bia
     kinds = _norm_kinds(kind, gate_kind)
     x = _rows(residual, "residual", shape, tr, device)
     if block is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=tr, device=residual.device)
+        residual_out = _dense_like(residual)
     if pre_gain is not None and normed is None:
-        normed = torch.empty(shape, dtype=dtype, device=residual.device)
+        normed = torch.empty(shape, dtype=dtype, device=residual.device) if block is None \
+            else _dense_like(block)
     v = (d,)
     _check(lib.sa_block_norm_forward(
         *x, *_rows(block, "block", shape, dtype, device), *_rows(gate, "gate", shape, dtype, device),
@@ -1005,18 +1012,18 @@ def block_norm_backward(residual_out, block, d_residual_out, d_normed, gate=None
               _vector(res_scale, "res_scale", v, f32, device),
               _vector(pre_gain, "pre_gain", v, f32, device),
               _vector(pre_bias, "pre_bias", v, f32, device)]
-    out = dict(d_residual=torch.empty(shape, dtype=tr, device=dev))
+    out = dict(d_residual=_dense_like(residual_out))
     if block is not None:
-        out["d_block"] = torch.empty(shape, dtype=dtype, device=dev)
+        out["d_block"] = _dense_like(block)
     if gate is not None:
-        out["d_gate"] = torch.empty(shape, dtype=dtype, device=dev)
+        out["d_gate"] = _dense_like(gate)
     sums = []
     for name, p in zip(("d_post_gain", "d_post_bias", "d_res_scale", "d_pre_gain", "d_pre_bias"),
                        params):
         if p is None:
             sums.append(None)
             continue
-        out[name] = torch.empty(v, dtype=f32, device=dev)
+        out[name] = torch.empty(d, dtype=f32, device=dev)
         sums.append(out[name].data_ptr())
     if workspace is None and any(sums):
         workspace = torch.empty(lib.sa_workspace_bytes_block_norm(rows, d) or 16, dtype=torch.uint8,
