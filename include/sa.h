@@ -642,8 +642,10 @@ sa_status sa_action_sketch_forward(sa_action act, sa_query q, const void* E, con
  * products with fp32 accumulation on the tensor cores; the weights of a
  * tile (q . k times the decay) and the copy of the state that outputs are
  * taken from are rounded to bf16, and the state itself is kept in fp32, its
- * sums formed from operands split into two bf16 parts.  SA_FP32: fp32
- * arithmetic on the CUDA cores.
+ * sums formed from operands split into two bf16 parts (three where a final
+ * state or a d_initial_state is asked for).  SA_FP32: fp32 arithmetic on the
+ * CUDA cores.  A value that is not finite reaches only the rows that the
+ * formula lets see it (and the state).
  *
  * Common arguments
  *   q, k, v     device; row t, head h of q starts at q + t * q_row + h *
@@ -656,8 +658,8 @@ sa_status sa_action_sketch_forward(sa_action act, sa_query q, const void* E, con
  *               SA_DEVFLAG_DECAY and counts as 0 or as -inf
  *   offsets     device, int64, batch + 1 entries: offsets[0] == 0,
  *               non-decreasing, offsets[batch] <= total_rows.  Rows behind
- *               offsets[batch] belong to nobody: they are not read, and
- *               their output rows are left as they were
+ *               offsets[batch] belong to nobody: what they hold does not
+ *               matter, and their output rows are left as they were
  *   batch       0 <= batch < 2^21
  *   total_rows  0 <= total_rows < 2^31 - 256
  *   max_rows    the longest history, if known, else 0: batches with few and

@@ -18,6 +18,8 @@
 // What bounds it: memory, one read for the norm, one read and one write for
 // the scaling.  Pass 2 walks each block's range backwards, so that it begins
 // with what pass 1 has left in L2; its stores are marked for early eviction.
+// Measured: 354 M bf16 values in 217 tensors: 387 us (130 + 228 us of device
+// time, 5.4 and 6.2 TB/s); 19 tensors of 0.5 M fp32 values: 5.4 us in a graph.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -26,7 +28,7 @@
 
 #include "sa.h"
 #include "sa_internal.h"
-#include "sa_ptx.cuh"
+#include "sa_operators.cuh"
 
 namespace sa {
 namespace {

@@ -206,13 +206,6 @@ bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t co
 bool make_tmap_bf16_box(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                         uint32_t box_cols, uint32_t box_rows, int swizzle_bytes);
 
-// 3-D bf16 tensor map over [rows][heads][d] with the given strides in
-// elements (multiples of 8, not 0): boxes of 64 columns x one head x box_rows
-// rows, 128-byte swizzle, zero fill.
-bool make_tmap_bf16_heads(CUtensorMap* m, const void* base, uint64_t rows, uint64_t heads,
-                          uint64_t d, uint64_t row_stride, uint64_t head_stride,
-                          uint32_t box_rows);
-
 // Action-side fusion (sa_action.cu): the width d and the device of a
 // prepared producer, and the producer kernel X = E + SwiGLU-FFN([E; a]) for
 // `rows` rows enqueued on `st` (flag bits OR-ed into *flags when not null).

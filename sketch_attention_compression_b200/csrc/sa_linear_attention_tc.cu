@@ -27,12 +27,19 @@
 // and warps 12-15, one row of the chunk per thread,
 //   s2  turn P into P~ (TMEM to TMEM), while M2 and s3 run
 //   s4  store the last 32 columns of out.
-// What bounds it: shared memory.  The products' operands, the split, the
-// state's copy and the loads move 560 KB per chunk at da = dc = 128, 4400
-// cycles at 128 bytes each, against 5500 cycles of its share of DRAM; the
-// rest of the time is the chain s1, M2, s3, M4.  With da = 64 the parts of
-// w b lie side by side, so that one product of N = 128 or 192 reads c once
-// for all of them.
+// What bounds it: the chain s1, M2, s3, M4 from chunk to chunk, some 7500
+// cycles at da = dc = 128 against 5500 for the chunk's share of DRAM.  No unit
+// is full (148 histories of 4096 rows at da = dc = 128: tensor pipe 35 % of
+// its cycles, issue slots 40 %, shared-memory pipe 36 %, DRAM 42 %), but the
+// products read 8 KB of shared memory every 64 cycles, all that it has, so
+// that they and s3 slow each other down where they meet: M4 by halves of the
+// rows, to start during s3, made a chunk 8 % longer.  Hence few bytes rather
+// than more overlap: with da = 64 the parts of w b lie side by side, and one
+// product of N = 128 or 192 reads c once for all of them.
+// Measured: 16 x 100K rows, two heads of 64: 0.80 ms (2.1 TB/s of its own
+// bytes), of which the segments' states take 0.23; 48 ragged histories of up
+// to 4099 rows, eight heads of 128: 0.18 ms (3.3 TB/s); backward of 16 x 10K
+// rows, eight heads of 128: 1.03-1.09 ms (2.2 TB/s).
 // TMEM: P and P~ at 0, O1 at 128, O2 at 256, D behind it.  Shared memory at
 // da = dc = 128: two stages of three 32 KB tiles and 32 KB for S~: 224 KB.
 //
@@ -44,7 +51,7 @@
 #include "sa.h"
 #include "sa_internal.h"
 #include "sa_linear_attention.h"
-#include "sa_ptx.cuh"
+#include "sa_operators.cuh"
 
 namespace sa {
 namespace {
