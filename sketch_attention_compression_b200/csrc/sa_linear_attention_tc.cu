@@ -17,12 +17,12 @@
 // long sums are not left to the accumulator's rounding.
 //
 // One persistent CTA per SM: warp 0 fetches work items and loads tiles (TMA,
-// two stages), warp 1 issues the MMAs.  Warps 4-11 hold the state, two warps
+// two or three stages), warp 1 issues the MMAs.  Warps 4-11 hold the state, two warps
 // per TMEM lane quarter, each with half of the columns; per chunk they
 //   s1  add D of the chunk before to S and store S~
-//   s3  split w b: into places of their own a chunk ahead (da = dc = 64),
-//       the first part over b once M1 has read it (da = 64), or also the
-//       others over a and in S~'s place once M2 has read those
+//   s3  split w b: into a place of its own (da = dc = 64), the first part
+//       over b once M1 has read it (da = 64), or also the others over a and
+//       in S~'s place once M2 has read those
 //   s4  store most columns of out, while M4 runs
 // and warps 12-15, one row of the chunk per thread,
 //   s2  turn P into P~ (TMEM to TMEM), while M2 and s3 run
@@ -58,24 +58,25 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kStateThreads = 256;  // warps 4-11
-constexpr int kStages = 2, kRing = 4;
+constexpr int kRing = 4;
 constexpr int kBox = 128 * 128;  // 128 rows x 64 bf16
 constexpr int kTable = 132;         // l^0 .. l^128, then l^128's rounding error
 
-template <int DA, int DC>
+template <int DA, int DC, bool STATE>
 struct TcPlan {
+  // The parts of w b.  da = dc = 64: a place of their own (two in turn for
+  // the states alone), and three stages of tiles; da = 64: the first one over
+  // b, the others behind it; else over b, over a and in S~'s place.
+  static constexpr bool kApart = DA == 64 && DC == 64, kOwn = DA == 64 && !kApart;
+  static constexpr int kStages = kApart ? 3 : 2;
   static constexpr int kA = 0;                          // within a stage
-  static constexpr int kB = kA + (DA / 64) * kBox;
-  // The parts of w b.  da = dc = 64: boxes of their own behind b; da = 64:
-  // the first one over b, the others behind it; else over b, over a and in
-  // S~'s place.
-  static constexpr bool kOwn = DA == 64, kApart = DA == 64 && DC == 64;
-  static constexpr int kHi = kApart ? kB + kBox : kB;
-  static constexpr int kC = kOwn ? kHi + 3 * kBox : kB + (DA / 64) * kBox;
+  static constexpr int kB = STATE && kApart ? 0 : kA + (DA / 64) * kBox;
+  static constexpr int kC = kB + (kOwn ? 3 : DA / 64) * kBox;
   static constexpr int kStage = kC + (DC / 64) * kBox;
-  static constexpr int kS = kStages * kStage;           // S~^T: da / 64 boxes of dc rows
+  static constexpr int kParts = kStages * kStage;       // (kApart)
+  static constexpr int kS = kParts + (kApart ? (STATE ? 6 : 3) * kBox : 0);  // S~^T: da / 64 boxes of dc rows
   static constexpr int kSBox = DC * 128;
-  static constexpr int kTab = kS + (kOwn ? kSBox : 2 * kBox);  // four tables of powers
+  static constexpr int kTab = kS + (DA == 64 ? kSBox : 2 * kBox);  // four tables of powers
   static constexpr int kItems = kTab + 4 * kTable * 4;
   static constexpr int kBars = kItems + kRing * 64;
   static constexpr int kUsed = kBars + 256;
@@ -203,8 +204,9 @@ __device__ __forceinline__ void store_out(const ScanPass& p, int heads, int head
 template <int DA, int DC, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1)
     scan_tc_kernel(const __grid_constant__ ScanMaps maps, const __grid_constant__ ScanArgs t) {
-  using Pl = TcPlan<DA, DC>;
+  using Pl = TcPlan<DA, DC, STATE>;
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int kStages = Pl::kStages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (blockIdx.x == 0 && tid == 0) {
@@ -219,21 +221,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (t.check && blockIdx.x == 0) check_inputs(t.s, reinterpret_cast<uint32_t*>(smem));
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Pl::kBars);
-  uint64_t* full = bars;                   // [2] a stage's tiles have landed
-  uint64_t* empty = bars + 2;              // [2] a stage's products are done
-  uint64_t* item_full = bars + 4;          // [4]
-  uint64_t* item_empty = bars + 8;         // [4]
-  uint64_t* p_full = bars + 12;            // M1 done
-  uint64_t* s_ready = bars + 13;           // S~ stored, D read
-  uint64_t* a_free = bars + 14;            // M2 done (and M1)
-  uint64_t* p_ready = bars + 15;           // P~ stored
-  uint64_t* b_ready = bars + 16;           // w b stored
-  uint64_t* o_full = bars + 17;            // M3 done (and M2)
-  uint64_t* d_full = bars + 18;            // [2] M4 done (chunks in turn)
-  uint64_t* o_read = bars + 20;            // warps 12-15 have read O1, O2
-  uint64_t* tab_ready = bars + 21;         // [2] a table of powers stored (state, weight warps)
-  uint64_t* drain = bars + 23;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  uint64_t* full = bars;                   // [3] a stage's tiles have landed
+  uint64_t* empty = bars + 3;              // [3] a stage's products are done
+  uint64_t* item_full = bars + 6;          // [4]
+  uint64_t* item_empty = bars + 10;        // [4]
+  uint64_t* p_full = bars + 14;            // M1 done
+  uint64_t* s_ready = bars + 15;           // S~ stored, D read
+  uint64_t* a_free = bars + 16;            // M2 done (and M1)
+  uint64_t* p_ready = bars + 17;           // P~ stored
+  uint64_t* b_ready = bars + 18;           // w b stored
+  uint64_t* o_full = bars + 19;            // M3 done (and M2)
+  uint64_t* d_full = bars + 20;            // [2] M4 done (chunks in turn)
+  uint64_t* o_read = bars + 22;            // warps 12-15 have read O1, O2
+  uint64_t* tab_ready = bars + 23;         // [2] a table of powers stored (state, weight warps)
+  uint64_t* drain = bars + 25;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -432,25 +434,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           // c^T times the parts of w b, both MN-major.
           const bool three = t.p[it.pass].parts == 3;
-          const uint64_t hi = smem_desc(d + Pl::kHi, kBox, 1024, 2);
+          const uint64_t hi = smem_desc(
+              Pl::kApart ? sbase + Pl::kParts + (STATE ? (n & 1u) * (3 * kBox) : 0) : d + Pl::kB, kBox, 1024, 2);
           auto product = [&](uint64_t part, uint32_t id, bool first) {
 #pragma unroll
             for (int g = 0; g < 2; ++g)
               group(d_col(n), cm + g * 4 * kStepMn, kStepMn, part + g * 4 * kStepMn, kStepMn, id,
                     first && g == 0);
           };
-          if (Pl::kOwn) {
+          if (DA == 64) {
             // One product for the parts side by side, 64 columns of D each;
             // with dc = 128 TMEM has room for two of them.
             product(hi, DC == 64 && three ? id_192 : id_128, true);
-            if (DC == 128 && three) product(smem_desc(d + Pl::kHi + 2 * kBox, kBox, 1024, 2), id_64, false);
+            if (DC == 128 && three) product(smem_desc(d + Pl::kB + 2 * kBox, kBox, 1024, 2), id_64, false);
           } else {
             product(hi, id_128, true);
             product(smem_desc(d + Pl::kA, kBox, 1024, 2), id_128, false);
             if (three) product(smem_desc(sbase + Pl::kS, kBox, 1024, 2), id_128, false);
           }
           mma_commit(empty + st);
-          mma_commit(d_full + st);
+          mma_commit(d_full + (n & 1u));
         }
         __syncwarp();
         if (!STATE && !Pl::kOwn) ahead_m1();
@@ -487,10 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < HA / 16; ++j) {
           uint32_t v[16], lo[16];
           tmem_ld16(d + j * 16, v);
-          if (Pl::kOwn) tmem_ld16(d + 64 + j * 16, lo);
+          if (DA == 64) tmem_ld16(d + 64 + j * 16, lo);
           tmem_wait_ld();
           tmem_pin16(v);
-          if (Pl::kOwn) {
+          if (DA == 64) {
             tmem_pin16(lo);
             if (DC == 64 && three) {
               uint32_t low[16];
@@ -541,19 +544,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++items;
       const int64_t chunks = (it.hi - it.lo + 127) / 128;
       float f = 0.f, fl = 0.f;  // decay of S over the chunk before
-      // s3 is early where its places do not depend on M2.
-      const bool early = Pl::kOwn || (STATE && p.parts == 2);
-      // With places apart it is done a chunk ahead, while M2 and M3 run.
-      constexpr bool kAhead = !STATE && Pl::kApart;
+      // s3 comes before s1 where its places are free by then.
+      const bool early = STATE ? DA == 64 || p.parts == 2 : Pl::kOwn;
       // s3: w b in two or three bf16 parts, for a chunk of L rows at d.
-      auto split = [&](uint32_t d, int L) {
+      auto split = [&](uint32_t d, int L, uint32_t m) {
         constexpr int kRowStep = kStateThreads / (DA / 8);  // a multiple of 8
         const int u = ctid % (DA / 8), first = ctid / (DA / 8);
         const uint32_t o = (u >> 3) * kBox + swz(first, u & 7);
         uint32_t src = d + Pl::kB + o;
-        uint32_t hi_dst = d + Pl::kHi + o;
-        uint32_t dst = Pl::kOwn ? hi_dst + kBox : d + Pl::kA + o;
-        uint32_t third = Pl::kOwn ? hi_dst + 2 * kBox : sbase + Pl::kS + o;
+        uint32_t hi_dst = Pl::kApart ? sbase + Pl::kParts + (STATE ? (m & 1u) * (3 * kBox) : 0) + o : src;
+        uint32_t dst = DA == 64 ? hi_dst + kBox : d + Pl::kA + o;
+        uint32_t third = DA == 64 ? hi_dst + 2 * kBox : sbase + Pl::kS + o;
         const bool three = p.parts == 3;
         const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll 2
@@ -605,8 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (early) {
-          if (!STATE && !Pl::kApart && !warp_wait(p_full, m & 1u, abort_flag, sticky)) return false;
-          split(d, L);
+          if (!STATE && !warp_wait(p_full, m & 1u, abort_flag, sticky)) return false;
+          split(d, L, m);
         }
         return true;
       };
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int L = static_cast<int>(it.hi - r0 < 128 ? it.hi - r0 : 128);
         // A reverse scan's first chunk of a user takes the start state undecayed.
         const int skip = rev && it.first && c == 0 ? 1 : 0;
-        if ((!kAhead || c == 0) && !tiles(c, n)) { ok = false; break; }
+        if (!tiles(c, n)) { ok = false; break; }
         if (STATE && early) {
           // Two places for D: the chunk before is added while M4 runs.
           fence_proxy_async_smem();
@@ -649,14 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           warp_arrive(s_ready, lane);
         }
         if (!early) {
-          if (!STATE && !warp_wait(a_free, ph, abort_flag, sticky)) { ok = false; break; }
-          split(d, L);
+          if (!STATE && !Pl::kApart && !warp_wait(a_free, ph, abort_flag, sticky)) { ok = false; break; }
+          split(d, L, n);
         }
         if (!STATE || !early) {
           fence_proxy_async_smem();
           warp_arrive(b_ready, lane);
         }
-        if (kAhead && c + 1 < chunks && !tiles(c + 1, n + 1)) { ok = false; break; }
         // s4
         if (!STATE) {
           if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int DA, int DC, bool STATE>
 cudaError_t launch(const ScanMaps& m, const ScanArgs& t, bool beside, int sms, cudaStream_t st) {
-  using Pl = TcPlan<DA, DC>;
+  using Pl = TcPlan<DA, DC, STATE>;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t err = allow_smem(scan_tc_kernel<DA, DC, STATE>, Pl::kSmem, allowed);
   if (err != cudaSuccess) return err;
