@@ -23,10 +23,12 @@
 //   s3  split w b: into a place of its own (da = dc = 64), the first part
 //       over b once M1 has read it (da = 64), or also the others over a and
 //       in S~'s place once M2 has read those
-//   s4  store most columns of out, while M4 runs
 // and warps 12-15, one row of the chunk per thread,
 //   s2  turn P into P~ (TMEM to TMEM), while M2 and s3 run
-//   s4  store the last 32 columns of out.
+//   s4  store out, while M4 runs.
+// (Warps 4-11 that stored a part of out too were slower, and so were eight
+// warps for the output: backward of 16 x 10K rows at eight heads of 128: 857
+// us, with 96 of 128 columns stored by warps 4-11 932, with 20 warps 969.)
 // What bounds it: the chain s1, M2, s3, M4 from chunk to chunk, some 7500
 // cycles at da = dc = 128 against 5500 for the chunk's share of DRAM.  No unit
 // is full (148 histories of 4096 rows at da = dc = 128: tensor pipe 35 % of
@@ -93,7 +95,6 @@ struct TcPlan {
 static_assert(sizeof(ScanItem) <= 64, "ring entry");
 
 constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256;
-constexpr int kSideCols = 32;  // columns of out that warps 12-15 store
 
 __device__ __forceinline__ uint32_t swz(int r, int u) {
   return (r >> 3) * 1024 + (r & 7) * 128 + ((u ^ (r & 7)) << 4);
@@ -657,15 +658,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           warp_arrive(b_ready, lane);
         }
-        // s4
-        if (!STATE) {
-          if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
-          tc_fence_after();
-          const float w1 = p.out_mul * power(row < L ? (rev ? L - row : row + 1) - skip : 0);
-          constexpr int kCols = (DC - kSideCols) / 2;
-          store_out<DC>(p, t.s.heads, it.head, r0, L, row, hf * kCols, kCols / 16, w1, lane_base, tab);
-          tc_fence_before();
-        }
       }
       if (!ok) break;
       if (chunks > 0) add_d(n - 1, f, fl, p.parts == 3);
@@ -773,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
         tc_fence_after();
         const float w1 = p.out_mul * power(row < L ? (rev ? L - row : row + 1) - skip : 0);
-        store_out<DC>(p, t.s.heads, it.head, r0, L, row, DC - kSideCols, kSideCols / 16, w1, lane_base, tab);
+        store_out<DC>(p, t.s.heads, it.head, r0, L, row, 0, DC / 16, w1, lane_base, tab);
         tc_fence_before();
         warp_arrive(o_read, lane);
       }
