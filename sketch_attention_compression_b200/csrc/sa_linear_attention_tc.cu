@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           // The next chunk's M1 goes before this chunk's M4 where s3 waits for
           // it, if its tiles are there.
-          if (Pl::kOwn) ahead_m1();
+          if (DA == 64) ahead_m1();
         }
         if (!warp_wait(b_ready, ph, abort_flag, sticky)) { ok = false; break; }
         tc_fence_after();
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(d_full + (n & 1u));
         }
         __syncwarp();
-        if (!STATE && !Pl::kOwn) ahead_m1();
+        if (!STATE && DA != 64) ahead_m1();
         ahead = next;
       }
     }
