@@ -753,6 +753,19 @@ def _stream_of(stream, device):
     return _stream_handle(stream)
 
 
+def _used_on(stream, *tensors):
+    """Tensors that a call allocated on the current stream and uses on
+    `stream`: their memory is not handed out again before it has been used."""
+    if stream is None:
+        return
+    torch = _torch()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _on_device(t, name, device):
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the current CUDA device")
@@ -849,6 +862,7 @@ def linear_attention_forward(q, k, v, log_decay, offsets, scale, initial_state=N
         _vector(final_state, "final_state", states, f32, device),
         *_buffer(workspace, "workspace", device), _stream_of(stream, device)),
         "sa_linear_attention_forward")
+    _used_on(stream, out, final_state, workspace)
     return out, final_state, workspace
 
 
@@ -881,6 +895,7 @@ def linear_attention_backward(q, k, v, log_decay, offsets, scale, d_out, initial
         out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(),
         None if ds0 is None else ds0.data_ptr(), *_buffer(workspace, "workspace", device),
         _stream_of(stream, device)), "sa_linear_attention_backward")
+    _used_on(stream, *out.values(), workspace)
     return out, workspace
 
 
@@ -908,6 +923,7 @@ def linear_attention_step(state, q, k, v, log_decay, scale, slots=None, out=None
         _vector(out, "out", (B, H, dv), dtype, device),
         _buffer(device_flags, "device_flags", device)[0], _stream_of(stream, device)),
         "sa_linear_attention_step")
+    _used_on(stream, out)
     return out
 
 
@@ -976,6 +992,7 @@ def block_norm_forward(residual, block=None, gate=None, post_gain=None, post_bia
         *kinds, float(eps), _dense(residual_out, "residual_out", shape, tr, device),
         _dense(normed, "normed", shape, dtype, device), _stream_of(stream, device)),
         "sa_block_norm_forward")
+    _used_on(stream, residual_out, normed)
     return residual_out, normed
 
 
@@ -1038,6 +1055,7 @@ def block_norm_backward(residual_out, block, d_residual_out, d_normed, gate=None
         _dense(out.get("d_gate"), "d_gate", shape, dtype, device), *sums,
         *_buffer(workspace, "workspace", device), _stream_of(stream, device)),
         "sa_block_norm_backward")
+    _used_on(stream, *out.values(), workspace)
     return out
 
 
@@ -1090,6 +1108,7 @@ def _clip(torch, lib, grads, max_norm, out, norm, workspace, device, stream):
     else:
         _check(lib.sa_clip_grad_norm(src, None if targets is None else targets.buffer_info()[0], num, typ,
                                      n, max_norm, *rest), "sa_clip_grad_norm")
+    _used_on(stream, norm, workspace)
     return norm
 
 

@@ -29,19 +29,20 @@
 // (Warps 4-11 that stored a part of out too were slower, and so were eight
 // warps for the output: backward of 16 x 10K rows at eight heads of 128: 857
 // us, with 96 of 128 columns stored by warps 4-11 932, with 20 warps 969.)
-// What bounds it: the chain s1, M2, s3, M4 from chunk to chunk, some 7500
-// cycles at da = dc = 128 against 5500 for the chunk's share of DRAM.  No unit
-// is full (148 histories of 4096 rows at da = dc = 128: tensor pipe 35 % of
-// its cycles, issue slots 40 %, shared-memory pipe 36 %, DRAM 42 %), but the
-// products read 8 KB of shared memory every 64 cycles, all that it has, so
-// that they and s3 slow each other down where they meet: M4 by halves of the
-// rows, to start during s3, made a chunk 8 % longer.  Hence few bytes rather
-// than more overlap: with da = 64 the parts of w b lie side by side, and one
-// product of N = 128 or 192 reads c once for all of them.
-// Measured: 16 x 100K rows, two heads of 64: 0.80 ms (2.1 TB/s of its own
-// bytes), of which the segments' states take 0.23; 48 ragged histories of up
-// to 4099 rows, eight heads of 128: 0.18 ms (3.3 TB/s); backward of 16 x 10K
-// rows, eight heads of 128: 1.03-1.09 ms (2.2 TB/s).
+// What bounds it: the chain s1, M2, s3, M4 from chunk to chunk, some 7000
+// cycles at da = dc = 128 (8500 with three parts) against 5500 for the chunk's
+// share of DRAM.  No unit is full (148 histories of 4096 rows at da = dc =
+// 128: tensor pipe 38 % of its cycles, issue slots 40 %, shared-memory pipe
+// 38 %, DRAM 49 %), but the products read 8 KB of shared memory every 64
+// cycles, all that it has, so that they and s3 slow each other down where they
+// meet: M4 by halves of the rows, to start during s3, made a chunk 8 % longer.
+// Code size counts too: unrolling s2's loop made it 40 % longer.  With da = 64
+// the parts of w b lie side by side, and one product of N = 128 or 192 reads c
+// once for all of them.
+// Measured: 16 x 100K rows, two heads of 64: 0.76 ms (2.2 TB/s of its own
+// bytes), of which the segments' states take 0.22; 48 ragged histories of up
+// to 4099 rows, eight heads of 128: 0.18 ms (3.4 TB/s); backward of 16 x 10K
+// rows, eight heads of 128: 0.89-1.0 ms (2.3-2.6 TB/s).
 // TMEM: P and P~ at 0, O1 at 128, O2 at 256, D behind it.  Shared memory at
 // da = dc = 128: two stages of three 32 KB tiles and 32 KB for S~: 224 KB.
 //

@@ -155,3 +155,43 @@ def test_a_prompt_then_single_rows():
     final = s["state"][users].double()
     assert (pool[slots].double() - final).norm() <= 2.0 ** -18 * final.norm()
     assert (pool[[1, 3, 4, 6]] == 3.0).all()
+
+
+def test_a_stream_of_its_own():
+    """Every operator on a stream that is given, as an object and as a handle,
+    while the current stream keeps taking and filling memory: what a call
+    allocates is not handed out again before that stream has used it."""
+    import torch
+    from sketch_attention_compression_b200 import (block_norm_backward, block_norm_forward,
+                                                   clip_grad_norm, linear_attention_backward,
+                                                   linear_attention_forward, linear_attention_step)
+    p, dr, du = _setup()
+    s, r, _ = _forward(p)
+    state = s["state"].clone()
+    big = torch.empty(1 << 26, device="cuda")
+
+    def calls(**kw):
+        y, f, _ = linear_attention_forward(s["q"], s["k"], s["v"], p["g"], p["off"], 0.125, **kw)
+        g, _ = linear_attention_backward(s["q"], s["k"], s["v"], p["g"], p["off"], 0.125, s["y"], **kw)
+        pool = state.clone()
+        torch.cuda.synchronize()
+        o = linear_attention_step(pool, s["q"][:5], s["k"][:5], s["v"][:5], p["g"], 0.125, **kw)
+        r1, u1 = block_norm_forward(p["x"], s["y"].view(-1, W), s["z"], post_gain=p["g_post"],
+                                    pre_gain=p["g_out"], gate_kind="silu", **kw)
+        b = block_norm_backward(r, s["y"].view(-1, W), dr, du, s["z"], post_gain=p["g_post"],
+                                pre_gain=p["g_out"], gate_kind="silu", **kw)
+        c = [p["x"].clone(), p["g_in"].clone()]
+        torch.cuda.synchronize()
+        n = clip_grad_norm(c, 1.0, **kw)
+        return [y, f, *g.values(), pool, o, r1, u1, *b.values(), *c, n]
+
+    want = calls()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            big.fill_(1.0)                       # keeps the side stream busy
+        got = calls(stream=stream)
+        rubbish = [torch.full((n,), 7.0, device="cuda") for n in (1 << 10, 1 << 14, 1 << 18)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del rubbish
