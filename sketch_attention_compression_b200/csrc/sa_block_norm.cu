@@ -38,7 +38,6 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "sa.h"
 #include "sa_internal.h"
