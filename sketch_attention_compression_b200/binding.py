@@ -9,6 +9,7 @@ fallback: if libsa.so is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -753,17 +754,33 @@ def _stream_of(stream, device):
     return _stream_handle(stream)
 
 
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _as_stream(stream):
+    """The torch stream of a stream object or handle."""
+    return stream if hasattr(stream, "cuda_stream") else _torch().cuda.ExternalStream(int(stream))
+
+
+def _allocating_on(stream):
+    """Tensors allocated in this context belong to `stream`, on which the call
+    runs: the allocator gives memory freed on a stream back to that stream at
+    once, so memory of the current one could still be in use by work queued
+    there when `stream` writes it."""
+    return _NO_STREAM if stream is None else _torch().cuda.stream(_as_stream(stream))
+
+
 def _used_on(stream, *tensors):
-    """Tensors that a call allocated on the current stream and uses on
-    `stream`: their memory is not handed out again before it has been used."""
+    """The outputs and the workspace of a call on `stream`: their memory is
+    not handed out again before that stream and the current one, on which the
+    caller may read them, are through with what they hold now."""
     if stream is None:
         return
-    torch = _torch()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+    stream, current = _as_stream(stream), _torch().cuda.current_stream()
     for t in tensors:
-        if t is not None:
+        if t is not None and t.numel() > 0:
             t.record_stream(stream)
+            t.record_stream(current)
 
 
 def _on_device(t, name, device):
@@ -838,6 +855,8 @@ def linear_attention_forward(q, k, v, log_decay, offsets, scale, initial_state=N
     fp32), strided as they come as long as the last dimension is contiguous;
     log_decay (H,) fp32; offsets (B + 1,) int64; initial_state (B, H, d_k,
     d_v) fp32 or None; max_rows a bound on the longest history, if known.
+    With a stream (object or handle) the call runs there, what it allocates
+    is that stream's memory, and ordering the inputs is the caller's part.
     Returns (out (N, H, d_v), final_state (B, H, d_k, d_v) fp32, workspace);
     final_state may be given as initial_state itself."""
     torch, lib = _torch(), load_library()
@@ -847,13 +866,14 @@ def linear_attention_forward(q, k, v, log_decay, offsets, scale, initial_state=N
     args = (*_strided(q, "q", (N, H, dk), dtype, device), *_strided(k, "k", (N, H, dk), dtype, device),
             *_strided(v, "v", (N, H, dv), dtype, device))
     bound = 0 if max_rows is None else int(max_rows)
-    if out is None:
-        out = _dense_like(v)
-    if final_state is None:
-        final_state = torch.empty(states, dtype=f32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
-                                dtype=torch.uint8, device=q.device)
+    with _allocating_on(stream):
+        if out is None:
+            out = _dense_like(v)
+        if final_state is None:
+            final_state = torch.empty(states, dtype=f32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
+                                    dtype=torch.uint8, device=q.device)
     _check(lib.sa_linear_attention_forward(
         *args, _vector(log_decay, "log_decay", (H,), f32, device), _buffer(offsets, "offsets", device)[0],
         B, N, bound, H, dk, dv, _dtype_code(dtype), float(scale),
@@ -880,13 +900,14 @@ def linear_attention_backward(q, k, v, log_decay, offsets, scale, d_out, initial
             *_strided(v, "v", (N, H, dv), dtype, device))
     grad = _strided(d_out, "d_out", (N, H, dv), dtype, device)
     bound = 0 if max_rows is None else int(max_rows)
-    out = dict(dq=_dense_like(q), dk=_dense_like(k), dv=_dense_like(v))
-    ds0 = None
-    if initial_state is not None:
-        ds0 = out["d_initial_state"] = _dense_like(initial_state)
-    if workspace is None:
-        workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
-                                dtype=torch.uint8, device=q.device)
+    with _allocating_on(stream):
+        out = dict(dq=_dense_like(q), dk=_dense_like(k), dv=_dense_like(v))
+        ds0 = None
+        if initial_state is not None:
+            ds0 = out["d_initial_state"] = _dense_like(initial_state)
+        if workspace is None:
+            workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
+                                    dtype=torch.uint8, device=q.device)
     _check(lib.sa_linear_attention_backward(
         *args, _vector(log_decay, "log_decay", (H,), f32, device), _buffer(offsets, "offsets", device)[0],
         B, N, bound, H, dk, dv, _dtype_code(dtype), float(scale),
@@ -915,7 +936,8 @@ def linear_attention_step(state, q, k, v, log_decay, scale, slots=None, out=None
     args = (*_strided(q, "q", (B, H, dk), dtype, device), *_strided(k, "k", (B, H, dk), dtype, device),
             *_strided(v, "v", (B, H, dv), dtype, device))
     if out is None:
-        out = _dense_like(v)
+        with _allocating_on(stream):
+            out = _dense_like(v)
     _check(lib.sa_linear_attention_step(
         *args, _vector(log_decay, "log_decay", (H,), f32, device),
         _vector(slots, "slots", (B,), torch.int64, device), B, S, H, dk, dv, _dtype_code(dtype), float(scale),
@@ -978,11 +1000,12 @@ def block_norm_forward(residual, block=None, gate=None, post_gain=None, post_bia
         dtype = tr
     kinds = _norm_kinds(kind, gate_kind)
     x = _rows(residual, "residual", shape, tr, device)
-    if block is not None and residual_out is None:
-        residual_out = _dense_like(residual)
-    if pre_gain is not None and normed is None:
-        normed = torch.empty(shape, dtype=dtype, device=residual.device) if block is None \
-            else _dense_like(block)
+    with _allocating_on(stream):
+        if block is not None and residual_out is None:
+            residual_out = _dense_like(residual)
+        if pre_gain is not None and normed is None:
+            normed = torch.empty(shape, dtype=dtype, device=residual.device) if block is None \
+                else _dense_like(block)
     v = (d,)
     _check(lib.sa_block_norm_forward(
         *x, *_rows(block, "block", shape, dtype, device), *_rows(gate, "gate", shape, dtype, device),
@@ -1029,22 +1052,23 @@ def block_norm_backward(residual_out, block, d_residual_out, d_normed, gate=None
               _vector(res_scale, "res_scale", v, f32, device),
               _vector(pre_gain, "pre_gain", v, f32, device),
               _vector(pre_bias, "pre_bias", v, f32, device)]
-    out = dict(d_residual=_dense_like(residual_out))
-    if block is not None:
-        out["d_block"] = _dense_like(block)
-    if gate is not None:
-        out["d_gate"] = _dense_like(gate)
-    sums = []
-    for name, p in zip(("d_post_gain", "d_post_bias", "d_res_scale", "d_pre_gain", "d_pre_bias"),
-                       params):
-        if p is None:
-            sums.append(None)
-            continue
-        out[name] = torch.empty(d, dtype=f32, device=dev)
-        sums.append(out[name].data_ptr())
-    if workspace is None and any(sums):
-        workspace = torch.empty(lib.sa_workspace_bytes_block_norm(rows, d) or 16, dtype=torch.uint8,
-                                device=dev)
+    with _allocating_on(stream):
+        out = dict(d_residual=_dense_like(residual_out))
+        if block is not None:
+            out["d_block"] = _dense_like(block)
+        if gate is not None:
+            out["d_gate"] = _dense_like(gate)
+        sums = []
+        for name, p in zip(("d_post_gain", "d_post_bias", "d_res_scale", "d_pre_gain", "d_pre_bias"),
+                           params):
+            if p is None:
+                sums.append(None)
+                continue
+            out[name] = torch.empty(d, dtype=f32, device=dev)
+            sums.append(out[name].data_ptr())
+        if workspace is None and any(sums):
+            workspace = torch.empty(lib.sa_workspace_bytes_block_norm(rows, d) or 16, dtype=torch.uint8,
+                                    device=dev)
     _check(lib.sa_block_norm_backward(
         *r, *_rows(block, "block", shape, dtype, device), *_rows(gate, "gate", shape, dtype, device),
         *params[:4], rows, d, _dtype_code(tr), _dtype_code(dtype), *kinds, float(eps),
@@ -1093,11 +1117,13 @@ def _clip(torch, lib, grads, max_norm, out, norm, workspace, device, stream):
         targets = array.array("Q", to)
     device = grads[0].device if n > 0 else device
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=device)
+        with _allocating_on(stream):
+            norm = torch.empty((), dtype=torch.float32, device=device)
     elif norm.dtype is not torch.float32 or norm.numel() != 1:
         raise ValueError("norm must hold one float32")
     if workspace is None:
-        workspace = torch.empty(lib.sa_workspace_bytes_grad_norm(n), dtype=torch.uint8, device=device)
+        with _allocating_on(stream):
+            workspace = torch.empty(lib.sa_workspace_bytes_grad_norm(n), dtype=torch.uint8, device=device)
     # Kept alive by name until the call has read them.
     table = array.array("Q", addresses), array.array("q", sizes), array.array("i", types)
     src, num, typ = (a.buffer_info()[0] for a in table)
