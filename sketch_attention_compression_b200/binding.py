@@ -175,6 +175,42 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _other_stream(stream):
+    """The torch stream of a stream object or handle; None for the current one."""
+    if stream is None:
+        return None
+    torch = _torch()
+    if _stream_handle(stream) == torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()):
+        return None
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+
+
+def _allocating_on(stream):
+    """Tensors allocated in this context belong to `stream`, on which the call
+    runs: the allocator gives memory freed on a stream back to that stream at
+    once, so memory of the current one could still be in use by work queued
+    there when `stream` writes it."""
+    other = _other_stream(stream)
+    return _NO_STREAM if other is None else _torch().cuda.stream(other)
+
+
+def _used_on(stream, *tensors):
+    """The outputs and the workspace of a call on `stream`: their memory is
+    not handed out again before that stream and the current one, on which the
+    caller may read them, are through with what they hold now."""
+    other = _other_stream(stream)
+    if other is None:
+        return
+    current = _torch().cuda.current_stream()
+    for t in tensors:
+        if t is not None and t.numel() > 0:
+            t.record_stream(other)
+            t.record_stream(current)
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     if t == torch.bfloat16:
@@ -232,7 +268,7 @@ class SketchQuery:
                            device=self.device)
 
     # -- device path -------------------------------------------------------
-    def _args(self, X, offsets, X_tilde, mass, workspace):
+    def _args(self, X, offsets, X_tilde, mass, workspace, stream):
         torch = _torch()
         if X.dtype != self.dtype:
             raise TypeError(f"X dtype {X.dtype} != query dtype {self.dtype}")
@@ -242,12 +278,13 @@ class SketchQuery:
             raise TypeError("offsets must be a 1-D int64 tensor")
         B = int(offsets.shape[0]) - 1
         N = int(X.shape[0])
-        if X_tilde is None:
-            X_tilde = torch.empty((B, self.k, self.d), dtype=torch.float32, device=X.device)
-        if mass is None:
-            mass = torch.empty((B, self.k), dtype=torch.float32, device=X.device)
-        if workspace is None:
-            workspace = self.new_workspace(B, N)
+        with _allocating_on(stream):
+            if X_tilde is None:
+                X_tilde = torch.empty((B, self.k, self.d), dtype=torch.float32, device=X.device)
+            if mass is None:
+                mass = torch.empty((B, self.k), dtype=torch.float32, device=X.device)
+            if workspace is None:
+                workspace = self.new_workspace(B, N)
         xp = ctypes.c_void_p(X.data_ptr()) if N > 0 else ctypes.c_void_p(0)
         if N > 0:
             _dev_ptr(X, "X")
@@ -259,9 +296,10 @@ class SketchQuery:
     def forward(self, X, offsets, X_tilde=None, mass=None, workspace=None, stream=None,
                 check: bool = False) -> Tuple[object, object]:
         """X~ (B, k, d) and m (B, k) for the ragged batch (X (N, d), offsets (B+1,))."""
-        args, X_tilde, mass, workspace = self._args(X, offsets, X_tilde, mass, workspace)
+        args, X_tilde, mass, workspace = self._args(X, offsets, X_tilde, mass, workspace, stream)
         sh = ctypes.c_void_p(_stream_handle(stream))
         _check(self._lib.sa_sketch_forward(self._h, *args, sh), "sa_sketch_forward")
+        _used_on(stream, X_tilde, mass, workspace)
         if check:
             read_device_status(workspace, stream)
         return X_tilde, mass
@@ -279,13 +317,15 @@ class SketchQuery:
         if queries.dtype != torch.float32 or tuple(queries.shape) != (B, self.k, self.d):
             raise ValueError(f"queries must be float32 of shape ({B}, {self.k}, {self.d})")
         if workspace is None:
-            workspace = torch.empty(self.workspace_bytes_user_queries(B, int(X.shape[0])),
-                                    dtype=torch.uint8, device=X.device)
-        args, X_tilde, mass, workspace = self._args(X, offsets, X_tilde, mass, workspace)
+            with _allocating_on(stream):
+                workspace = torch.empty(self.workspace_bytes_user_queries(B, int(X.shape[0])),
+                                        dtype=torch.uint8, device=X.device)
+        args, X_tilde, mass, workspace = self._args(X, offsets, X_tilde, mass, workspace, stream)
         qp = _dev_ptr(queries, "queries") if B > 0 else ctypes.c_void_p(0)
         sh = ctypes.c_void_p(_stream_handle(stream))
         _check(self._lib.sa_sketch_forward_user_queries(self._h, qp, *args, sh),
                "sa_sketch_forward_user_queries")
+        _used_on(stream, X_tilde, mass, workspace)
         if check:
             read_device_status(workspace, stream)
         return X_tilde, mass
@@ -293,18 +333,18 @@ class SketchQuery:
     def partials_user_queries(self, queries, X, offsets, X_tilde, mass, workspace,
                               stream=None) -> None:
         """Q'_b and the fused pass of forward_user_queries (finalize() completes it)."""
-        args, *_ = self._args(X, offsets, X_tilde, mass, workspace)
+        args, *_ = self._args(X, offsets, X_tilde, mass, workspace, stream)
         _check(self._lib.sa_sketch_partials_user_queries(
             self._h, _dev_ptr(queries, "queries"), *args, ctypes.c_void_p(_stream_handle(stream))),
             "sa_sketch_partials_user_queries")
 
     def partials(self, X, offsets, X_tilde, mass, workspace, stream=None) -> None:
-        args, *_ = self._args(X, offsets, X_tilde, mass, workspace)
+        args, *_ = self._args(X, offsets, X_tilde, mass, workspace, stream)
         _check(self._lib.sa_sketch_partials(self._h, *args, ctypes.c_void_p(_stream_handle(stream))),
                "sa_sketch_partials")
 
     def finalize(self, X, offsets, X_tilde, mass, workspace, stream=None) -> None:
-        args, *_ = self._args(X, offsets, X_tilde, mass, workspace)
+        args, *_ = self._args(X, offsets, X_tilde, mass, workspace, stream)
         _check(self._lib.sa_sketch_finalize(self._h, *args, ctypes.c_void_p(_stream_handle(stream))),
                "sa_sketch_finalize")
 
@@ -324,10 +364,11 @@ class SketchQuery:
             raise TypeError("offsets must be a 1-D int64 tensor")
         B = int(offsets.shape[0]) - 1
         N = int(X.shape[0])
-        if X_tilde is None:
-            X_tilde = torch.empty((B, self.k, self.d), dtype=torch.float32, device=X.device)
-        if mass is None:
-            mass = torch.empty((B, self.k), dtype=torch.float32, device=X.device)
+        with _allocating_on(stream):
+            if X_tilde is None:
+                X_tilde = torch.empty((B, self.k, self.d), dtype=torch.float32, device=X.device)
+            if mass is None:
+                mass = torch.empty((B, self.k), dtype=torch.float32, device=X.device)
         xp = _dev_ptr(X, "X") if N > 0 else ctypes.c_void_p(0)
         fp = ctypes.c_void_p(0)
         if device_flags is not None:
@@ -338,6 +379,7 @@ class SketchQuery:
             self._h, xp, _dev_ptr(offsets, "offsets"), B, N, _dev_ptr(X_tilde, "X_tilde"),
             _dev_ptr(mass, "mass"), fp, ctypes.c_void_p(_stream_handle(stream)))
         _check(st, "sa_sketch_forward_noalloc")
+        _used_on(stream, X_tilde, mass)
         return X_tilde, mass
 
     # -- host path ---------------------------------------------------------
@@ -357,8 +399,9 @@ class SketchQuery:
             raise ValueError("X_host must be a contiguous CPU tensor of the query dtype")
         N = int(X_host.shape[0])
         if device_buffer is None:
-            device_buffer = torch.empty(self.host_path_device_bytes(B, N), dtype=torch.uint8,
-                                        device=self.device)
+            with _allocating_on(stream):
+                device_buffer = torch.empty(self.host_path_device_bytes(B, N), dtype=torch.uint8,
+                                            device=self.device)
         if out_x is None:
             out_x = np.empty((B, self.k, self.d), dtype=np.float32)
         if out_m is None:
@@ -370,6 +413,7 @@ class SketchQuery:
             _dev_ptr(device_buffer, "device_buffer"),
             int(device_buffer.numel()), ctypes.c_void_p(_stream_handle(stream)))
         _check(st, "sa_sketch_forward_host")
+        _used_on(stream, device_buffer)
         return out_x, out_m
 
     def backward(self, X, offsets, G, g=None, P_f32=None, W_Q_f32=None, W_K_f32=None,
@@ -381,14 +425,15 @@ class SketchQuery:
         dQueries (B, k, d), dW_Q, dW_K (d, d)) and the workspace."""
         torch = _torch()
         B, N = int(offsets.shape[0]) - 1, int(X.shape[0])
-        dX = torch.empty((N, self.d), dtype=torch.bfloat16, device=X.device)
-        dP = torch.empty((self.k, self.d) if queries is None else (B, self.k, self.d),
-                         dtype=torch.float32, device=X.device)
-        dWQ = torch.empty((self.d, self.d), dtype=torch.float32, device=X.device)
-        dWK = torch.empty_like(dWQ)
-        if workspace is None:
-            workspace = torch.empty(int(self._lib.sa_workspace_bytes_backward(self._h, B, N)),
-                                    dtype=torch.uint8, device=X.device)
+        with _allocating_on(stream):
+            dX = torch.empty((N, self.d), dtype=torch.bfloat16, device=X.device)
+            dP = torch.empty((self.k, self.d) if queries is None else (B, self.k, self.d),
+                             dtype=torch.float32, device=X.device)
+            dWQ = torch.empty((self.d, self.d), dtype=torch.float32, device=X.device)
+            dWK = torch.empty_like(dWQ)
+            if workspace is None:
+                workspace = torch.empty(int(self._lib.sa_workspace_bytes_backward(self._h, B, N)),
+                                        dtype=torch.uint8, device=X.device)
         opt = lambda t, n: _dev_ptr(t, n) if t is not None else ctypes.c_void_p(0)  # noqa: E731
         _check(self._lib.sa_sketch_backward(
             self._h, opt(queries, "queries"), opt(P_f32, "P_f32"), _dev_ptr(W_Q_f32, "W_Q_f32"),
@@ -398,6 +443,7 @@ class SketchQuery:
             _dev_ptr(dWQ, "dW_Q"), _dev_ptr(dWK, "dW_K"), _dev_ptr(workspace, "workspace"),
             int(workspace.numel() * workspace.element_size()),
             ctypes.c_void_p(_stream_handle(stream))), "sa_sketch_backward")
+        _used_on(stream, dX, dP, dWQ, dWK, workspace)
         out = dict(dX=dX, dW_Q=dWQ, dW_K=dWK)
         out["dP" if queries is None else "dQueries"] = dP
         return out, workspace
@@ -445,13 +491,15 @@ class RefineParams:
         torch = _torch()
         B, k, d = (int(x) for x in X_tilde.shape)
         if out is None:
-            out = torch.empty_like(X_tilde)
+            with _allocating_on(stream):
+                out = torch.empty_like(X_tilde)
         fp = _dev_ptr(device_flags, "device_flags") if device_flags is not None else ctypes.c_void_p(0)
         _check(self._lib.sa_refine_update(self._h, _dev_ptr(prev, "prev"), int(prev_shared),
                                           _dev_ptr(X_tilde, "X_tilde"), _dev_ptr(mass, "mass"), B, k,
                                           _dev_ptr(out, "out"), fp,
                                           ctypes.c_void_p(_stream_handle(stream))),
                "sa_refine_update")
+        _used_on(stream, out)
         return out
 
     def close(self) -> None:
@@ -473,11 +521,12 @@ def refine_layer_forward(query: "SketchQuery", params: RefineParams, X, offsets,
     torch = _torch()
     lib = load_library()
     B, N = int(offsets.shape[0]) - 1, int(X.shape[0])
-    if out is None:
-        out = torch.empty((B, query.k, query.d), dtype=torch.float32, device=X.device)
-    if workspace is None:
-        workspace = torch.empty(int(lib.sa_workspace_bytes_refine_layer(query._h, B, N)),
-                                dtype=torch.uint8, device=X.device)
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty((B, query.k, query.d), dtype=torch.float32, device=X.device)
+        if workspace is None:
+            workspace = torch.empty(int(lib.sa_workspace_bytes_refine_layer(query._h, B, N)),
+                                    dtype=torch.uint8, device=X.device)
     _check(lib.sa_refine_layer_forward(
         query._h, params._h, _dev_ptr(prev, "prev") if prev is not None else ctypes.c_void_p(0),
         _dev_ptr(P_f32, "P_f32") if P_f32 is not None else ctypes.c_void_p(0),
@@ -485,6 +534,7 @@ def refine_layer_forward(query: "SketchQuery", params: RefineParams, X, offsets,
         _dev_ptr(out, "out"), _dev_ptr(workspace, "workspace"),
         int(workspace.numel() * workspace.element_size()),
         ctypes.c_void_p(_stream_handle(stream))), "sa_refine_layer_forward")
+    _used_on(stream, out, workspace)
     return out, workspace
 
 
@@ -499,11 +549,12 @@ def refine_stack_forward(queries, params, P_f32, X, offsets, out=None, workspace
         raise ValueError("one query and one parameter set per layer")
     B, N = int(offsets.shape[0]) - 1, int(X.shape[0])
     q0 = queries[0]
-    if out is None:
-        out = torch.empty((B, q0.k, q0.d), dtype=torch.float32, device=X.device)
-    if workspace is None:
-        workspace = torch.empty(int(lib.sa_workspace_bytes_refine_stack(q0._h, B, N)),
-                                dtype=torch.uint8, device=X.device)
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty((B, q0.k, q0.d), dtype=torch.float32, device=X.device)
+        if workspace is None:
+            workspace = torch.empty(int(lib.sa_workspace_bytes_refine_stack(q0._h, B, N)),
+                                    dtype=torch.uint8, device=X.device)
     qs = (ctypes.c_void_p * L)(*[q._h.value for q in queries])
     rs = (ctypes.c_void_p * L)(*[r._h.value for r in params])
     _check(lib.sa_refine_stack_forward(
@@ -512,6 +563,7 @@ def refine_stack_forward(queries, params, P_f32, X, offsets, out=None, workspace
         _dev_ptr(offsets, "offsets"), B, N, _dev_ptr(out, "out"),
         _dev_ptr(workspace, "workspace"), int(workspace.numel() * workspace.element_size()),
         ctypes.c_void_p(_stream_handle(stream))), "sa_refine_stack_forward")
+    _used_on(stream, out, workspace)
     return out, workspace
 
 
@@ -526,11 +578,13 @@ def mass_normalise(X_tilde, mass, out=None, stream=None):
     if tuple(mass.shape) != (B, k):
         raise ValueError("mass must be (B, k)")
     if out is None:
-        out = torch.empty_like(X_tilde)
+        with _allocating_on(stream):
+            out = torch.empty_like(X_tilde)
     if B > 0:
         _check(lib.sa_mass_normalise(_dev_ptr(X_tilde, "X_tilde"), _dev_ptr(mass, "mass"), B, k, d,
                                      _dev_ptr(out, "out"), ctypes.c_void_p(_stream_handle(stream))),
                "sa_mass_normalise")
+        _used_on(stream, out)
     return out
 
 
@@ -593,13 +647,14 @@ class SketchCache:
         B, N = int(offsets_host.shape[0]) - 1, int(X.shape[0])
         if len(keys) != B:
             raise ValueError("one key per user")
-        if X_tilde is None:
-            X_tilde = torch.empty((B, self.k, self.d), dtype=torch.float32, device=X.device)
-        if mass is None:
-            mass = torch.empty((B, self.k), dtype=torch.float32, device=X.device)
-        if workspace is None:
-            workspace = torch.empty(int(self._lib.sa_cache_forward_workspace_bytes(query._h, B, N)),
-                                    dtype=torch.uint8, device=X.device)
+        with _allocating_on(stream):
+            if X_tilde is None:
+                X_tilde = torch.empty((B, self.k, self.d), dtype=torch.float32, device=X.device)
+            if mass is None:
+                mass = torch.empty((B, self.k), dtype=torch.float32, device=X.device)
+            if workspace is None:
+                workspace = torch.empty(int(self._lib.sa_cache_forward_workspace_bytes(query._h, B, N)),
+                                        dtype=torch.uint8, device=X.device)
         hit = np.zeros(max(B, 1), dtype=np.uint8)
         _check(self._lib.sa_cache_forward(
             self._h, query._h, _keys_array(keys).ctypes.data_as(ctypes.c_void_p), float(now),
@@ -608,6 +663,7 @@ class SketchCache:
             _dev_ptr(mass, "mass"), hit.ctypes.data_as(ctypes.c_void_p),
             _dev_ptr(workspace, "workspace"), int(workspace.numel() * workspace.element_size()),
             ctypes.c_void_p(_stream_handle(stream))), "sa_cache_forward")
+        _used_on(stream, X_tilde, mass, workspace)
         return X_tilde, mass, hit[:B].astype(bool), workspace
 
     def close(self) -> None:
@@ -645,13 +701,15 @@ class WidthAdapter:
             raise TypeError("X_tilde must be float32 with last dimension d")
         rows = int(X_tilde.numel()) // self.d
         if out is None:
-            out = torch.empty(tuple(X_tilde.shape[:-1]) + (self.D,), dtype=torch.bfloat16,
-                              device=X_tilde.device)
+            with _allocating_on(stream):
+                out = torch.empty(tuple(X_tilde.shape[:-1]) + (self.D,), dtype=torch.bfloat16,
+                                  device=X_tilde.device)
         fp = _dev_ptr(device_flags, "device_flags") if device_flags is not None else ctypes.c_void_p(0)
         _check(self._lib.sa_adapter_forward(self._h, _dev_ptr(X_tilde, "X_tilde"), rows,
                                              _dev_ptr(out, "out"), fp,
                                              ctypes.c_void_p(_stream_handle(stream))),
                "sa_adapter_forward")
+        _used_on(stream, out)
         return out
 
     def close(self) -> None:
@@ -695,13 +753,15 @@ class ActionFusion:
             raise TypeError("E must be bfloat16 and types uint8")
         rows = int(E.shape[0])
         if out is None:
-            out = torch.empty_like(E)
+            with _allocating_on(stream):
+                out = torch.empty_like(E)
         fp = _dev_ptr(device_flags, "device_flags") if device_flags is not None else ctypes.c_void_p(0)
         if rows > 0:
             _check(self._lib.sa_action_fuse(self._h, _dev_ptr(E, "E"), _dev_ptr(types, "types"), rows,
                                             _dev_ptr(out, "out"), fp,
                                             ctypes.c_void_p(_stream_handle(stream))),
                    "sa_action_fuse")
+            _used_on(stream, out)
         return out
 
     def sketch_forward(self, query: "SketchQuery", E, types, offsets, X_tilde=None, mass=None,
@@ -710,19 +770,21 @@ class ActionFusion:
         Returns (X_tilde, mass, workspace)."""
         torch = _torch()
         B, N = int(offsets.shape[0]) - 1, int(E.shape[0])
-        if X_tilde is None:
-            X_tilde = torch.empty((B, query.k, query.d), dtype=torch.float32, device=E.device)
-        if mass is None:
-            mass = torch.empty((B, query.k), dtype=torch.float32, device=E.device)
-        if workspace is None:
-            workspace = torch.empty(int(self._lib.sa_workspace_bytes_action_sketch(query._h, B, N)),
-                                    dtype=torch.uint8, device=E.device)
+        with _allocating_on(stream):
+            if X_tilde is None:
+                X_tilde = torch.empty((B, query.k, query.d), dtype=torch.float32, device=E.device)
+            if mass is None:
+                mass = torch.empty((B, query.k), dtype=torch.float32, device=E.device)
+            if workspace is None:
+                workspace = torch.empty(int(self._lib.sa_workspace_bytes_action_sketch(query._h, B, N)),
+                                        dtype=torch.uint8, device=E.device)
         _check(self._lib.sa_action_sketch_forward(
             self._h, query._h, ctypes.c_void_p(E.data_ptr() if N > 0 else 0),
             ctypes.c_void_p(types.data_ptr() if N > 0 else 0), _dev_ptr(offsets, "offsets"), B, N,
             _dev_ptr(X_tilde, "X_tilde"), _dev_ptr(mass, "mass"), _dev_ptr(workspace, "workspace"),
             int(workspace.numel() * workspace.element_size()),
             ctypes.c_void_p(_stream_handle(stream))), "sa_action_sketch_forward")
+        _used_on(stream, X_tilde, mass, workspace)
         return X_tilde, mass, workspace
 
     def close(self) -> None:
@@ -752,35 +814,6 @@ def _stream_of(stream, device):
     if stream is None:
         return _torch()._C._cuda_getCurrentRawStream(device)
     return _stream_handle(stream)
-
-
-_NO_STREAM = contextlib.nullcontext()
-
-
-def _as_stream(stream):
-    """The torch stream of a stream object or handle."""
-    return stream if hasattr(stream, "cuda_stream") else _torch().cuda.ExternalStream(int(stream))
-
-
-def _allocating_on(stream):
-    """Tensors allocated in this context belong to `stream`, on which the call
-    runs: the allocator gives memory freed on a stream back to that stream at
-    once, so memory of the current one could still be in use by work queued
-    there when `stream` writes it."""
-    return _NO_STREAM if stream is None else _torch().cuda.stream(_as_stream(stream))
-
-
-def _used_on(stream, *tensors):
-    """The outputs and the workspace of a call on `stream`: their memory is
-    not handed out again before that stream and the current one, on which the
-    caller may read them, are through with what they hold now."""
-    if stream is None:
-        return
-    stream, current = _as_stream(stream), _torch().cuda.current_stream()
-    for t in tensors:
-        if t is not None and t.numel() > 0:
-            t.record_stream(stream)
-            t.record_stream(current)
 
 
 def _on_device(t, name, device):

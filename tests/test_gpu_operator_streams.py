@@ -56,19 +56,23 @@ def _apart(spans, others):
                                   "clip"])
 @pytest.mark.parametrize("as_handle", [False, True])
 def test_memory_of_a_call_on_another_stream(name, as_handle, monkeypatch):
+    _memory_of_a_call(_calls()[name], _inputs, as_handle, monkeypatch)
+
+
+def _memory_of_a_call(call, make, as_handle, monkeypatch):
     import torch
     from sketch_attention_compression_b200 import binding
-    call, taken, used_on = _calls()[name], [], binding._used_on
+    taken, used_on = [], binding._used_on
 
     def spy(stream, *tensors):
         taken.extend(t for t in tensors if t is not None and t.numel() > 0)
         used_on(stream, *tensors)
 
     monkeypatch.setattr(binding, "_used_on", spy)
-    want = [t.clone() for t in call(_inputs(), None)]
+    want = [t.clone() for t in call(make(), None)]
     sizes = [(t.shape, t.dtype) for t in taken]
     taken.clear()
-    first, second = _inputs(), _inputs()
+    first, second = make(), make()
     side = torch.cuda.Stream()
     given = side.cuda_stream if as_handle else side
     # Memory that is free again on the current stream, and still read there.
@@ -116,3 +120,64 @@ def test_a_captured_call_on_a_forked_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def _layer_inputs():
+    import torch
+    from sketch_attention_compression_b200 import ActionFusion, RefineParams, SketchQuery, WidthAdapter
+    from synthetic import action_params, action_types, refine_params, upstream_gradients
+    from synthetic.workloads import make_inputs
+    i = make_inputs([700, 0, 129], d=128, k=64, dtype="bf16", seed=97)
+    layer, act = refine_params(128, 256, seed=96), action_params(128, 32, 128, 4, seed=98)
+
+    def f32(a):
+        return torch.from_numpy(a).float().cuda()
+
+    def bf16(a):
+        return f32(a).to(torch.bfloat16)
+
+    G, g = upstream_gradients(3, 64, 128, seed=95)
+    names = ("W1", "W3", "W2", "gamma1", "beta1", "gamma2", "beta2")
+    return dict(X=bf16(i["X"]), host_offsets=i["offsets"], off=torch.from_numpy(i["offsets"]).cuda(),
+                q=SketchQuery(bf16(i["P"]), bf16(i["W_Q"]), bf16(i["W_K"]), i["scale"]),
+                Q=f32(i["P"]).expand(3, 64, 128).contiguous(), P=f32(i["P"]), WQ=f32(i["W_Q"]),
+                WK=f32(i["W_K"]), G=f32(G), gm=f32(g), sketch=f32(G), mass=f32(g).abs() + 1.0,
+                params=RefineParams(*(f32(layer[n]) for n in names)),
+                adapter=WidthAdapter(torch.full((128, 256), 0.125, device="cuda")),
+                action=ActionFusion(*(f32(act[n]) for n in ("W1", "W3", "W2", "table"))),
+                types=torch.from_numpy(action_types(len(i["X"]), 4, seed=97)).cuda())
+
+
+def _layer_calls():
+    from sketch_attention_compression_b200 import (SketchCache, mass_normalise, refine_layer_forward,
+                                                   refine_stack_forward)
+    keys = [(b, 1, 100, 7) for b in range(3)]
+
+    def cached(i, s):
+        i["cache"] = SketchCache(64, 128, capacity=4, ttl=60.0)
+        return i["cache"].forward(i["q"], keys, 0.0, i["X"], i["host_offsets"], stream=s)[:2]
+
+    return dict(
+        sketch=lambda i, s: i["q"].forward(i["X"], i["off"], stream=s),
+        user_queries=lambda i, s: i["q"].forward_user_queries(i["Q"], i["X"], i["off"], stream=s),
+        noalloc=lambda i, s: i["q"].forward_noalloc(i["X"], i["off"], stream=s),
+        backward=lambda i, s: list(i["q"].backward(
+            i["X"], i["off"], i["G"], i["gm"], P_f32=i["P"], W_Q_f32=i["WQ"], W_K_f32=i["WK"],
+            stream=s)[0].values()),
+        update=lambda i, s: [i["params"].update(i["Q"], i["sketch"], i["mass"], stream=s)],
+        layer=lambda i, s: [refine_layer_forward(i["q"], i["params"], i["X"], i["off"], P_f32=i["P"],
+                                                 stream=s)[0]],
+        stack=lambda i, s: [refine_stack_forward([i["q"]] * 2, [i["params"]] * 2, i["P"], i["X"],
+                                                 i["off"], stream=s)[0]],
+        normalise=lambda i, s: [mass_normalise(i["sketch"], i["mass"], stream=s)],
+        cached=cached,
+        adapter=lambda i, s: [i["adapter"].forward(i["sketch"].view(-1, 128), stream=s)],
+        fuse=lambda i, s: [i["action"].fuse(i["X"], i["types"], stream=s)],
+        action_sketch=lambda i, s: i["action"].sketch_forward(i["q"], i["X"], i["types"], i["off"],
+                                                              stream=s)[:2])
+
+
+@pytest.mark.parametrize("name", ["sketch", "user_queries", "noalloc", "backward", "update", "layer",
+                                  "stack", "normalise", "cached", "adapter", "fuse", "action_sketch"])
+def test_memory_of_a_layer_call_on_another_stream(name, monkeypatch):
+    _memory_of_a_call(_layer_calls()[name], _layer_inputs, False, monkeypatch)
