@@ -184,6 +184,7 @@ __device__ __forceinline__ void store_out(const ScanPass& p, int heads, int head
     if (odd_row) *reinterpret_cast<uint4*>(o + stride) = make_uint4(z[4], z[5], z[6], z[7]);
     if (__any_sync(0xFFFFFFFFu, f0 != 0.f || f1 != 0.f)) {
       uint16_t* own_row = static_cast<uint16_t*>(p.out) + (r0 + row) * stride + head * DC + col;
+      __syncwarp();  // half of the row's 16 values were stored by the other lane of the pair
 #pragma unroll 1
       for (int e = 0; e < 16; ++e) {
         uint32_t own, share;
