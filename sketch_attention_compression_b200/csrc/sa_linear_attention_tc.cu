@@ -47,8 +47,10 @@
 // da = dc = 128: two stages of three 32 KB tiles and 32 KB for S~: 224 KB.
 //
 // A product of P~ = 0 with a c that is not finite is NaN, so a row could see
-// such a value in its future.  An output whose O1 is not finite although
-// the state's share is, is summed again over the rows that it may see.
+// such a value in its future.  An output whose O1 is not finite although the
+// state's share is no NaN is summed again over the rows that it may see
+// (sum_again): in the first chunk of a user and head that holds such a value,
+// as the state carries it into every later one.
 #include <cuda_bf16.h>
 
 #include "sa.h"
@@ -104,23 +106,118 @@ __device__ __forceinline__ uint32_t swz(int r, int u) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// O1 of one output, over the rows that the scan has reached: for outputs that
-// values behind the mask have spoiled.
-__device__ __forceinline__ float masked_sum(const ScanPass& p, int head, int64_t r0, int L, int i,
-                                            int col, uint32_t powers) {
-  auto at = [&](const ScanInput& in, int r, int c) {
-    return bf_lo(static_cast<const uint16_t*>(
-        in.p)[(r0 + r) * in.row + static_cast<int64_t>(head) * in.head + c]);
-  };
-  float sum = 0.f;
+// The pairs of eight bf16.
+__device__ __forceinline__ void widen8(uint4 w, float (&v)[8]) {
+  v[0] = bf_lo(w.x), v[1] = bf_hi(w.x), v[2] = bf_lo(w.y), v[3] = bf_hi(w.y);
+  v[4] = bf_lo(w.z), v[5] = bf_hi(w.z), v[6] = bf_lo(w.w), v[7] = bf_hi(w.w);
+}
+
+// Sums the outputs of a warp's 32 rows again, in fp32 and over the rows that
+// the scan has reached only, where O1 is not finite and O2 is no NaN
+// (`batches`: a bit per 16 columns of this thread's row with such an O1).  A
+// row's weights are taken once and kept where O1 was: 128 columns of TMEM
+// that this warp's lanes own until o_read.  Bound by the latency of loads
+// from L2: about 150 us for a chunk at da = dc = 128, against 4 of any other
+// chunk (64 users of 512 rows with a row of NaN each, four heads, forward and
+// backward: 180 us without, 1200 to 1400 with).  Four weights at a time: 16
+// take a third less here, but that much code, though never run, made scans
+// without such values 1 to 2 % slower.
+template <int DC>
+__device__ __forceinline__ void sum_again(const ScanPass& p, int heads, int head, int64_t r0, int L, int row,
+                                       uint32_t batches, float w1, uint32_t lane_base, uint32_t powers) {
+  __syncwarp();  // the pair's other lane has stored half of this row
+  uint32_t todo = 0u;
 #pragma unroll 1
-  for (int j = p.reverse ? i : 0; j < (p.reverse ? L : i + 1); ++j) {
-    float x = 0.f;
-#pragma unroll 1
-    for (int d = 0; d < p.da; ++d) x = fmaf(at(p.a, i, d), at(p.b, j, d), x);
-    sum = fmaf(x * ld_shared_f32(powers + (p.reverse ? j - i : i - j) * 4), at(p.c, j, col), sum);
+  for (int b = 0; b < DC / 16; ++b) {
+    if (!__any_sync(0xFFFFFFFFu, (batches >> b) & 1u)) continue;
+    uint32_t x[16], y[16];
+    tmem_ld16(lane_base + kColO1 + b * 16, x);
+    tmem_ld16(lane_base + kColO2 + b * 16, y);
+    tmem_wait_ld();
+    tmem_pin16(x);
+    tmem_pin16(y);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (!isfinite(__uint_as_float(x[e])) && !isnan(__uint_as_float(y[e]))) todo |= 1u << b;
   }
-  return sum;
+  if (row >= L) todo = 0u;
+  if (!__any_sync(0xFFFFFFFFu, todo)) return;
+  auto line = [&](const ScanInput& in, int r) {  // a row of the chunk (16-byte aligned)
+    return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(in.p) + (r0 + r) * in.row +
+                                          static_cast<int64_t>(head) * in.head);
+  };
+  const bool rev = p.reverse != 0;
+  const int base = row & ~31;  // the warp's rows
+  const int j0 = rev ? base : 0, j1 = rev ? L : (base + 32 < L ? base + 32 : L);
+  const uint4* a = line(p.a, row < L ? row : L - 1);
+#pragma unroll 1
+  for (int j = j0; j < j1; j += 4) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int d = 0; d < p.da / 8; ++d) {
+      float u[8], v[8];
+      widen8(__ldg(a + d), u);
+      const uint4* b = line(p.b, j) + d;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        widen8(j + e < L ? __ldg(b) : make_uint4(0u, 0u, 0u, 0u), v);
+        b += p.b.row / 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[e] = fmaf(u[i], v[i], x[e]);
+      }
+    }
+    // A row that sees a NaN weight is NaN in every column, as it was stored.
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int dist = rev ? j + e - row : row - j - e;
+      if (dist >= 0 && isnan(x[e])) todo = 0u;
+      tmem_st1(lane_base + kColO1 + j + e,
+               dist >= 0 && j + e < L
+                   ? __float_as_uint(x[e] * (p.out_mul * ld_shared_f32(powers + dist * 4)))
+                   : 0u);
+    }
+  }
+  tmem_wait_st();
+  uint16_t* out = static_cast<uint16_t*>(p.out) +
+                  ((r0 + row) * static_cast<int64_t>(heads) + head) * DC;
+#pragma unroll 1
+  for (int b = 0; b < DC / 16; ++b) {
+    const bool mine = (todo >> b) & 1u;
+    if (!__any_sync(0xFFFFFFFFu, mine)) continue;
+    float o[16];
+    uint32_t y[16];
+    tmem_ld16(lane_base + kColO2 + b * 16, y);
+    tmem_wait_ld();
+    tmem_pin16(y);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = w1 * __uint_as_float(y[e]);
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+      const uint4* c = line(p.c, j) + b * 2;  // j < L
+      uint4 lo = __ldg(c), hi = __ldg(c + 1);
+      uint32_t w;
+      tmem_ld1(lane_base + kColO1 + j, w);
+      tmem_wait_ld();
+      tmem_pin1(w);
+      // A weight of 0 would not keep out what is not finite.
+      if (rev ? j < row : j > row) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+      float v[8];
+      widen8(lo, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(__uint_as_float(w), v[e], o[e]);
+      widen8(hi, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[8 + e] = fmaf(__uint_as_float(w), v[e], o[8 + e]);
+    }
+    if (mine) {
+      uint32_t z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+      uint4* q = reinterpret_cast<uint4*>(out + b * 16);
+      q[0] = make_uint4(z[0], z[1], z[2], z[3]);
+      q[1] = make_uint4(z[4], z[5], z[6], z[7]);
+    }
+  }
 }
 
 // The powers of exp(*log_decay) that one thread of a table's takes.
@@ -143,18 +240,19 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();  // the other lanes' next wait must not hold the arrival up
 }
 
-// Columns [col, col + 16 batches) of one row of out, from TMEM: O1 + w1 O2.
+// One row of out, from TMEM: O1 + w1 O2.
 template <int DC>
 __device__ __forceinline__ void store_out(const ScanPass& p, int heads, int head, int64_t r0, int L,
-                                          int row, int col, int batches, float w1,
-                                          uint32_t lane_base, uint32_t powers) {
+                                          int row, float w1, uint32_t lane_base, uint32_t powers) {
   const bool odd = (row & 1) != 0;
   const uint64_t w2 = f2_pack(w1, w1);
   const int64_t stride = static_cast<int64_t>(heads) * DC;
-  uint16_t* o = static_cast<uint16_t*>(p.out) + (r0 + (row & ~1)) * stride + head * DC + col + (odd ? 8 : 0);
+  uint16_t* o = static_cast<uint16_t*>(p.out) + (r0 + (row & ~1)) * stride + head * DC + (odd ? 8 : 0);
   const bool even_row = (row & ~1) < L, odd_row = (row | 1) < L;
+  uint32_t spoiled = 0u;
 #pragma unroll 1
-  for (int b = 0; b < batches; ++b, col += 16, o += 16) {
+  for (int b = 0; b < DC / 16; ++b, o += 16) {
+    const int col = b * 16;
     uint32_t x[16], y[16], z[8];
     tmem_ld16(lane_base + kColO1 + col, x);
     tmem_ld16(lane_base + kColO2 + col, y);
@@ -182,26 +280,10 @@ __device__ __forceinline__ void store_out(const ScanPass& p, int heads, int head
     }
     if (even_row) *reinterpret_cast<uint4*>(o) = make_uint4(z[0], z[1], z[2], z[3]);
     if (odd_row) *reinterpret_cast<uint4*>(o + stride) = make_uint4(z[4], z[5], z[6], z[7]);
-    if (__any_sync(0xFFFFFFFFu, f0 != 0.f || f1 != 0.f)) {
-      uint16_t* own_row = static_cast<uint16_t*>(p.out) + (r0 + row) * stride + head * DC + col;
-      __syncwarp();  // half of the row's 16 values were stored by the other lane of the pair
-#pragma unroll 1
-      for (int e = 0; e < 16; ++e) {
-        uint32_t own, share;
-        tmem_ld1(lane_base + kColO1 + col + e, own);
-        tmem_ld1(lane_base + kColO2 + col + e, share);
-        tmem_wait_ld();
-        tmem_pin1(own);
-        tmem_pin1(share);
-        if (row < L && !isfinite(__uint_as_float(own)) && isfinite(__uint_as_float(share)))
-          own_row[e] = static_cast<uint16_t>(
-              pack_bf16x2(fmaf(w1, __uint_as_float(share),
-                               p.out_mul * masked_sum(p, head, r0, L, row, col + e, powers)),
-                          0.f));
-        __syncwarp();
-      }
-    }
+    if (f0 != 0.f || f1 != 0.f) spoiled |= 1u << b;
   }
+  if (__any_sync(0xFFFFFFFFu, spoiled))
+    sum_again<DC>(p, heads, head, r0, L, row, spoiled, w1, lane_base, powers);
 }
 
 template <int DA, int DC, bool STATE>
@@ -767,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(o_full, ph, abort_flag, sticky)) { ok = false; break; }
         tc_fence_after();
         const float w1 = p.out_mul * power(row < L ? (rev ? L - row : row + 1) - skip : 0);
-        store_out<DC>(p, t.s.heads, it.head, r0, L, row, 0, DC / 16, w1, lane_base, tab);
+        store_out<DC>(p, t.s.heads, it.head, r0, L, row, w1, lane_base, tab);
         tc_fence_before();
         warp_arrive(o_read, lane);
       }

@@ -90,3 +90,55 @@ def test_single_values_stay_in_their_column(dk, dv, dtype, bad):
     # dv multiplies q into its weights: every column of the rows up to it
     assert not np.isfinite(got["dv"][:151, 1]).any()
     assert (np.abs(got["dv"] - want["dv"])[151:] <= TOL[dtype] * mag["dv"][151:] + 1e-36).all()
+
+
+@pytest.mark.parametrize("key", ["k", "v"])
+@pytest.mark.parametrize("row", [0, 127, 128, 255])
+def test_whole_rows_at_both_ends_of_a_chunk(key, row):
+    """A row of NaN or infinities: the rows before it are right, those from it
+    on are not finite, and the call does not become much slower."""
+    import torch
+    for bad in (float("nan"), float("inf")):
+        x = _make([256, 40], 2, 128, 128, "bf16", seed=row)
+        w = _np(x)
+        x[key][row] = bad
+        w[key][row] = 0.0
+        a = {name: np.abs(t) for name, t in w.items()}
+        want, _ = linear_attention(w["q"], w["k"], w["v"], w["g"], w["off"], 0.125)
+        mag, _ = linear_attention(a["q"], a["k"], a["v"], w["g"], w["off"], 0.125)
+        got, _ = _forward(x)
+        ok = np.r_[0:row, 256:296]
+        assert (np.abs(got - want)[ok] <= TOL["bf16"] * mag[ok] + 1e-36).all()
+        assert not np.isfinite(got[row:256]).any()
+
+
+@pytest.mark.parametrize("key,row", [("k", 0), ("k", 127), ("v", 0), ("v", 127), ("q", 0),
+                                     ("do", 127)])
+def test_time_with_rows_that_are_not_finite(key, row):
+    """64 users of 512 rows, each with one such row.  The chunk that holds it
+    is summed again at some 40 times the time of a chunk: with four chunks a
+    user the call may take some ten times as long.  A row's weights taken anew
+    for each of its 128 outputs would be 128 times as many."""
+    import torch
+    from sketch_attention_compression_b200 import linear_attention_backward, linear_attention_forward
+    x = _make([512] * 64, 4, 128, 128, "bf16", seed=1)
+    y = {name: t.cuda() for name, t in x.items()}
+    z = {name: t.clone() for name, t in y.items()}
+    z[key].view(64, 512, 4, 128)[:, 128 + row] = float("nan")
+
+    def best(t):
+        times = []
+        for _ in range(5):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            args = (t["q"], t["k"], t["v"], t["g"], t["off"], 0.125)
+            linear_attention_forward(*args, max_rows=512)
+            linear_attention_backward(*args, t["do"], max_rows=512)
+            e[1].record()
+            torch.cuda.synchronize()
+            times.append(e[0].elapsed_time(e[1]))
+        return min(times)
+
+    finite, spoiled = best(y), best(z)
+    print(f"{key} {row}: {finite * 1e3:.0f} us, {spoiled * 1e3:.0f} us with NaN")
+    assert spoiled <= 30 * finite
