@@ -851,8 +851,8 @@ sa_status sa_block_norm_backward(const void* residual_out, int64_t ld_residual, 
  *   max_norm    finite, >= 0
  *
  * Squares are summed in fp64 over the whole range of fp32, in a fixed order
- * (bitwise reproducible).  If the norm is not finite the values are left
- * (copied) as they are and *norm says so.
+ * (bitwise reproducible).  If *norm is not finite, also because finite values
+ * have a norm beyond fp32, the values are left (copied) as they are.
  */
 size_t sa_workspace_bytes_grad_norm(int64_t tensors);
 sa_status sa_grad_norm(const void* const* grads, const int64_t* numel, const sa_dtype* dtypes,

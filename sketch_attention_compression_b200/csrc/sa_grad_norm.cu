@@ -166,11 +166,12 @@ __global__ void __launch_bounds__(kClipThreads)
   __shared__ double buf[kClipThreads / 32];
   grid_dependency_wait();
   const double n = total_norm(part, parts, buf);
-  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(n);
-  // A norm that is not finite leaves the values as they are: the caller
-  // sees it in `norm`, and in the gradients where it came from.
+  const float told = static_cast<float>(n);
+  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = told;
+  // A norm that is not finite in fp32, as the caller sees it, leaves the
+  // values as they are.
   const double c = max_norm / (n + 1e-6);
-  const float m = isfinite(n) && c < 1.0 ? static_cast<float>(c) : 1.f;
+  const float m = isfinite(told) && c < 1.0 ? static_cast<float>(c) : 1.f;
   const int64_t c0 = t.chunks * blockIdx.x / gridDim.x;
   const int64_t c1 = t.chunks * (blockIdx.x + 1) / gridDim.x;
   if (c0 >= c1) return;
