@@ -170,8 +170,12 @@ __global__ void __launch_bounds__(kClipThreads)
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = told;
   // A norm that is not finite in fp32, as the caller sees it, leaves the
   // values as they are.
-  const double c = max_norm / (n + 1e-6);
-  const float m = isfinite(told) && c < 1.0 ? static_cast<float>(c) : 1.f;
+  const double factor = max_norm / (n + 1e-6);
+  const float m = isfinite(told) && factor < 1.0 ? static_cast<float>(factor) : 1.f;
+  // A factor below the smallest normal fp32 has fewer bits there, or none:
+  // products are then taken in 64 bits, element by element (a call on 354 M
+  // bf16 values: 852 us instead of 379).
+  const bool fine = isfinite(told) && factor < 0x1p-126 && factor != 0.0;
   const int64_t c0 = t.chunks * blockIdx.x / gridDim.x;
   const int64_t c1 = t.chunks * (blockIdx.x + 1) / gridDim.x;
   if (c0 >= c1) return;
@@ -185,6 +189,17 @@ __global__ void __launch_bounds__(kClipThreads)
     c = first;
     if (m == 1.f && g.dst == g.src) continue;
     const bool bf = g.n < 0;
+    if (fine) {
+      for (int64_t e = lo + threadIdx.x; e < hi; e += kClipThreads) {
+        if (bf)
+          static_cast<__nv_bfloat16*>(g.dst)[e] = __float2bfloat16_rn(static_cast<float>(
+              static_cast<double>(__bfloat162float(static_cast<const __nv_bfloat16*>(g.src)[e])) * factor));
+        else
+          static_cast<float*>(g.dst)[e] =
+              static_cast<float>(static_cast<double>(static_cast<const float*>(g.src)[e]) * factor);
+      }
+      continue;
+    }
     const bool vec = ((reinterpret_cast<uintptr_t>(g.src) | reinterpret_cast<uintptr_t>(g.dst)) & 15u) == 0;
     const int64_t units = vec ? (hi - lo) / (bf ? 8 : 4) : 0;
     const int64_t done = lo + units * (bf ? 8 : 4);
