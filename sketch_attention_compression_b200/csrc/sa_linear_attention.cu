@@ -1,6 +1,7 @@
 // Linear attention with a decay per head: the C entry points, the CUDA-core
 // scan and the single-step kernel.  The formulas are in sa_linear_attention.h.
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
 
 #include "sa.h"
@@ -145,7 +146,13 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
   const int64_t slot = a.slots != nullptr ? a.slots[b] : b;
   const bool padded = slot < 0, past = slot >= a.states, in_pool = !padded && !past;
   const float gd = a.log_decay[h];
-  const float l = expf(usable_decay(gd));
+  // The decay with its rounding error, which has one sign at every step and
+  // would add up over the horizon of a state that is advanced row by row.
+  const double w = exp(static_cast<double>(usable_decay(gd)));
+  const float l = static_cast<float>(w), ll = static_cast<float>(w - l);
+  auto next = [&](float x, float kv) {  // (an infinite x times ll = 0 would be NaN)
+    return fmaf(l, x, fmaf(ll, fminf(fmaxf(x, -FLT_MAX), FLT_MAX), kv));
+  };
   float* st = a.state + (((in_pool ? slot : 0) * a.heads + h) * a.dk) * a.dv + col;
   const T* vp = static_cast<const T*>(a.v.p) + b * a.v.row + h * a.v.head + col;
   float v[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -192,10 +199,10 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
       if (!live || r >= a.dk) continue;
       const float kv = sk[r], qv = sq[r];
       float4 x = s[i];
-      x.x = fmaf(kv, v[0], l * x.x);
-      x.y = fmaf(kv, v[1], l * x.y);
-      x.z = fmaf(kv, v[2], l * x.z);
-      x.w = fmaf(kv, v[3], l * x.w);
+      x.x = next(x.x, kv * v[0]);
+      x.y = next(x.y, kv * v[1]);
+      x.z = next(x.z, kv * v[2]);
+      x.w = next(x.w, kv * v[3]);
       *reinterpret_cast<float4*>(st + static_cast<int64_t>(r) * a.dv) = x;
       o[0] = fmaf(qv, x.x, o[0]);
       o[1] = fmaf(qv, x.y, o[1]);
