@@ -233,7 +233,10 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* buf, int& phase) {
   }
 }
 
-// 1 / (1 + exp(-z)) of a pair.
+// 1 / (1 + exp(-z)) of a pair.  The exponential and the reciprocal are the
+// approximate ones: a relative error of some (|z| + 8) 2^-24, most of it from
+// rounding z log2(e).  With expf and a division the forward over 200K x 1024
+// takes 540 us instead of 394.
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
   float a, b;
   f2_unpack(f2_mul(z, both(-1.4426950408889634f)), a, b);
@@ -252,14 +255,24 @@ __device__ __forceinline__ void gate_values(uint64_t (&z)[NV][kPairs], int kind)
       z[j][e] = kind == 1 ? s : f2_mul(z[j][e], s);
     }
 }
-// act'(z), and act(z) in `act`.
+// act'(z), and act(z) in `act`.  With t = exp(-|z|) and r = 1 / (1 + t) the
+// factors s and 1 - s of the slope are r and t r, swapped by the sign of z: 1
+// minus a rounded s would lose all of the slope's bits by z = 17.
 __device__ __forceinline__ uint64_t gate_slope(uint64_t z, int kind, uint64_t& act) {
-  const uint64_t one = both(1.f), minus = both(-1.f);
+  const uint64_t one = both(1.f);
   if (kind == 0) {
     act = z;
     return one;
   }
-  const uint64_t s = sigmoid2(z), rest = f2_fma(minus, s, one);  // 1 - s
+  float a, b, za, zb;
+  f2_unpack(z, za, zb);
+  f2_unpack(f2_mul(f2_pack(fabsf(za), fabsf(zb)), both(-1.4426950408889634f)), a, b);
+  const uint64_t t = f2_pack(ex2_approx(a), ex2_approx(b));
+  f2_unpack(f2_add(t, one), a, b);
+  const float r0 = rcp_approx(a), r1 = rcp_approx(b);
+  f2_unpack(f2_mul(t, f2_pack(r0, r1)), a, b);
+  const uint64_t s = f2_pack(za < 0.f ? a : r0, zb < 0.f ? b : r1);
+  const uint64_t rest = f2_pack(za < 0.f ? r0 : a, zb < 0.f ? r1 : b);  // 1 - s
   if (kind == 1) {
     act = s;
     return f2_mul(s, rest);
