@@ -660,7 +660,8 @@ sa_status sa_action_sketch_forward(sa_action act, sa_query q, const void* E, con
  *               non-decreasing, offsets[batch] <= total_rows.  Rows behind
  *               offsets[batch] belong to nobody: what they hold does not
  *               matter, and their output rows are left as they were
- *   batch       0 <= batch < 2^21
+ *   batch       0 <= batch < 2^21; with 0 nothing is launched, and the
+ *               workspace's flags stay as they were
  *   total_rows  0 <= total_rows < 2^31 - 256
  *   max_rows    the longest history, if known, else 0: batches with few and
  *               long histories are split along the rows, and a bound saves

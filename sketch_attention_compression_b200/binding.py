@@ -907,6 +907,8 @@ def linear_attention_forward(q, k, v, log_decay, offsets, scale, initial_state=N
         if workspace is None:
             workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
                                     dtype=torch.uint8, device=q.device)
+        if B == 0:
+            workspace[:8] = 0  # nothing is launched that would set the call's flags
     _check(lib.sa_linear_attention_forward(
         *args, _vector(log_decay, "log_decay", (H,), f32, device), _buffer(offsets, "offsets", device)[0],
         B, N, bound, H, dk, dv, _dtype_code(dtype), float(scale),
@@ -941,6 +943,8 @@ def linear_attention_backward(q, k, v, log_decay, offsets, scale, d_out, initial
         if workspace is None:
             workspace = torch.empty(lib.sa_workspace_bytes_linear_attention(H, dk, dv, B, N, bound) or 256,
                                     dtype=torch.uint8, device=q.device)
+        if B == 0:
+            workspace[:8] = 0  # nothing is launched that would set the call's flags
     _check(lib.sa_linear_attention_backward(
         *args, _vector(log_decay, "log_decay", (H,), f32, device), _buffer(offsets, "offsets", device)[0],
         B, N, bound, H, dk, dv, _dtype_code(dtype), float(scale),
