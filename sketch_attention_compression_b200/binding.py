@@ -962,13 +962,16 @@ def linear_attention_step(state, q, k, v, log_decay, scale, slots=None, out=None
     """One row for each of B stored states (sa_linear_attention_step), which
     are updated in place.  state (S, H, d_k, d_v) fp32; q, k (B, H, d_k) and
     v (B, H, d_v) bf16 or fp32; slots (B,) int64: the state of each entry (a
-    negative slot marks a padded entry), or None for entry b's state b.
-    Returns out (B, H, d_v)."""
+    negative slot marks a padded entry), or None for entry b's state b;
+    device_flags a CUDA tensor of at least one uint32 word, into which the
+    call's flags are OR-ed.  Returns out (B, H, d_v)."""
     torch, lib = _torch(), load_library()
     dtype, f32, device = q.dtype, torch.float32, _current_device(torch)
     B, H, dk, dv, _ = _attention_shapes(q, v, None)
     if state.dim() != 4:
         raise ValueError("state must be (states, heads, d_k, d_v)")
+    if device_flags is not None and device_flags.numel() * device_flags.element_size() < 4:
+        raise ValueError("device_flags must hold one uint32 word")
     S = state.shape[0]
     args = (*_strided(q, "q", (B, H, dk), dtype, device), *_strided(k, "k", (B, H, dk), dtype, device),
             *_strided(v, "v", (B, H, dv), dtype, device))
