@@ -32,9 +32,16 @@
 // single-element loads at columns R apart, so that neighbouring threads read
 // neighbouring elements.
 // Measured: forward over 200K x 1024 bf16 with both norms, SiLU gate and
-// scale: 390-415 us (5.1 TB/s; 69 % of the issue slots used before the packed
-// arithmetic); backward over 400K x 128, fp32 residual: 242-254 us (4.5
-// TB/s; three blocks of 128 threads per SM, by registers).
+// scale: 390-419 us (5.0 TB/s; 68 % of the issue slots); backward over 400K x
+// 128, fp32 residual: 242-261 us (4.4 TB/s; 50 % of the issue slots, with
+// three blocks of 128 threads per SM, by registers).
+// Far from memory's time: rows without 16-byte accesses, which are bound by
+// instructions (backward over 100K x 300 bf16: 626 us, 65 % of the issue slots,
+// where its bytes take 73), and the backward above 4096 columns, whose two
+// groups per thread do not fit its registers (20K x 8192: 1.4 ms, where its
+// bytes take 0.40; a launch over 5000 rows moves 2.2 GB to and from local
+// memory, beside 0.7 GB of DRAM).  The column sums add up to some hundreds of
+// rows per thread in fp32, then the blocks' sums in fp64.
 #include <cuda_bf16.h>
 
 #include <atomic>

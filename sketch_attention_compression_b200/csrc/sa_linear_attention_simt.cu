@@ -9,13 +9,18 @@
 // it, in shared memory.  Every product is a register-tiled one: 16 x 16
 // threads, operands read as 16-byte vectors.
 //
-// What bounds it: the fp32 pipe.  A chunk costs 64 da 64 (P) + half of
-// 64 64 dc (P c, the other half is zero and skipped) + 2 * 64 da dc
-// multiply-adds.  Tiles of 64 rows: P's cost grows with the tile, the number
-// of passes over the state with its inverse, and at da = dc = 128 the five
-// arrays fill 183 KB.  Measured: 16 x 100K rows, two heads of 64, forward:
-// 8.6 ms; 48 ragged histories of up to 4099
-// rows, eight heads of 128: 3.3 ms.
+// A chunk costs 64 da 64 (P) + half of 64 64 dc (P c, the other half is zero
+// and skipped) + 2 * 64 da dc multiply-adds.  Tiles of 64 rows: P's cost grows
+// with the tile, the number of passes over the state with its inverse, and at
+// da = dc = 128 the five arrays fill 183 KB.
+// What bounds it: latency.  The eight warps of an SM's one block wait for the
+// chunk's operands, which are loaded element by element between two barriers
+// with nothing in flight meanwhile, and for shared memory: 148 histories of
+// 2048 rows at da = dc = 64 keep the fp32 pipe busy for 35 % of its cycles,
+// the issue slots for 48 %, DRAM for 8 %.  Measured: 16 x 100K rows, two heads
+// of 64, forward: 6.9-8.6 ms; 48 ragged histories of up to 4099 rows, eight
+// heads of 128: 2.8-3.3 ms; backward of 16 x 10K rows, eight heads of 128:
+// 14-16 ms.
 #include <cuda_bf16.h>
 
 #include "sa.h"

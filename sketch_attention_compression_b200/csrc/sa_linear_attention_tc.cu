@@ -10,7 +10,9 @@
 //       out = O1 + mul l^(r+1) O2;  S <- l^L S + D
 //
 // Roundings to bf16: P~ and S~, the operands of an output that is bf16
-// itself.  S^T is kept in fp32 registers: w b is split into bf16 parts whose
+// itself.  They take its error from 1.7e-3 (its own rounding) to 2.3e-3 of its
+// 2-norm; second parts would double M2 and M3, and at da = dc = 128 there is
+// no shared memory for S~'s.  S^T is kept in fp32 registers: w b is split into bf16 parts whose
 // products are all accumulated, three parts (24 significant bits) where the
 // state itself is an answer, two (16 bits) where only S~ is taken from it;
 // each chunk's D starts from zero and is added to S in registers, so that
@@ -39,10 +41,11 @@
 // Code size counts too: unrolling s2's loop made it 40 % longer.  With da = 64
 // the parts of w b lie side by side, and one product of N = 128 or 192 reads c
 // once for all of them.
-// Measured: 16 x 100K rows, two heads of 64: 0.76 ms (2.2 TB/s of its own
-// bytes), of which the segments' states take 0.22; 48 ragged histories of up
-// to 4099 rows, eight heads of 128: 0.18 ms (3.4 TB/s); backward of 16 x 10K
-// rows, eight heads of 128: 0.89-1.0 ms (2.3-2.6 TB/s).
+// Measured: 16 x 100K rows, two heads of 64: 0.72-0.80 ms (2.1-2.3 TB/s of its
+// own bytes), of which the segments' states take 0.22; 48 ragged histories of
+// up to 4099 rows, eight heads of 128: 0.16-0.18 ms (3.3-3.7 TB/s), 0.14
+// without final states (two parts); backward of 16 x 10K rows, eight heads of
+// 128: 0.89-1.04 ms (2.2-2.6 TB/s).
 // TMEM: P and P~ at 0, O1 at 128, O2 at 256, D behind it.  Shared memory at
 // da = dc = 128: two stages of three 32 KB tiles and 32 KB for S~: 224 KB.
 //
