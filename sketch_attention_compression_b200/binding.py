@@ -180,8 +180,6 @@ _NO_STREAM = contextlib.nullcontext()
 
 def _other_stream(stream):
     """The torch stream of a stream object or handle; None for the current one."""
-    if stream is None:
-        return None
     torch = _torch()
     if _stream_handle(stream) == torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()):
         return None
@@ -193,16 +191,16 @@ def _allocating_on(stream):
     runs: the allocator gives memory freed on a stream back to that stream at
     once, so memory of the current one could still be in use by work queued
     there when `stream` writes it."""
-    other = _other_stream(stream)
-    return _NO_STREAM if other is None else _torch().cuda.stream(other)
+    if stream is None or (other := _other_stream(stream)) is None:
+        return _NO_STREAM
+    return _torch().cuda.stream(other)
 
 
 def _used_on(stream, *tensors):
     """The outputs and the workspace of a call on `stream`: their memory is
     not handed out again before that stream and the current one, on which the
     caller may read them, are through with what they hold now."""
-    other = _other_stream(stream)
-    if other is None:
+    if stream is None or (other := _other_stream(stream)) is None:
         return
     current = _torch().cuda.current_stream()
     for t in tensors:
@@ -1156,13 +1154,12 @@ def _clip(torch, lib, grads, max_norm, out, norm, workspace, device, stream):
             raise ValueError("out must match grads in number, shapes and types")
         targets = array.array("Q", to)
     device = grads[0].device if n > 0 else device
-    if norm is None:
-        with _allocating_on(stream):
-            norm = torch.empty((), dtype=torch.float32, device=device)
-    elif norm.dtype is not torch.float32 or norm.numel() != 1:
+    if norm is not None and (norm.dtype is not torch.float32 or norm.numel() != 1):
         raise ValueError("norm must hold one float32")
-    if workspace is None:
-        with _allocating_on(stream):
+    with _allocating_on(stream):
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=device)
+        if workspace is None:
             workspace = torch.empty(lib.sa_workspace_bytes_grad_norm(n), dtype=torch.uint8, device=device)
     # Kept alive by name until the call has read them.
     table = array.array("Q", addresses), array.array("q", sizes), array.array("i", types)
