@@ -1,6 +1,6 @@
 """Operators on a stream that is given: what a call allocates is neither
 memory that work queued on the current stream still uses, nor handed out
-again while the given stream uses it.  Addresses are compared, so a wrong
+again while the given stream, or the current one, uses it.  Addresses are compared, so a wrong
 allocation shows whether or not two kernels happen to meet in it."""
 
 import pytest
@@ -102,6 +102,23 @@ def _memory_of_a_call(call, make, as_handle, monkeypatch):
     assert _apart(spans, [_span(t) for t in new])
     torch.cuda.synchronize()
     assert all(bool((t == 9).all()) for t in new)
+    # Results that the current stream reads, and that are dropped meanwhile.
+    third, fourth = make(), make()
+    torch.cuda.synchronize()
+    got = call(third, given)
+    side.synchronize()
+    spans = [_span(t) for t in taken]
+    copies = [torch.empty_like(t) for t in got]
+    torch.cuda._sleep(BUSY)
+    for c, t in zip(copies, got):
+        c.copy_(t)
+    del got, t
+    taken.clear()
+    got = call(fourth, given)
+    assert _apart(spans, [_span(t) for t in taken])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copies, want))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_a_captured_call_on_a_forked_stream():
