@@ -127,9 +127,69 @@ struct StepArgs {
   int cols4;               // four-column groups per block
   float mul;
   uint32_t* flags;         // may be null
+  int marked;              // mark_kernel has gone before
 };
 
 constexpr int kStepThreads = 256, kStepBatch = 8, kStepMaxWidth = 256;
+// Of entries with equal slots the first is taken, a later one raises the
+// flag.  Up to this many blocks, each looks through the earlier entries' slots
+// while its state arrives; above, mark_kernel does so once per entry, not per
+// head, and leaves the answer where the entry's output goes.  Eight heads of
+// 64 x 64: 2000 entries 127 us (comparing) and 129 (marked), 4000: 260 and 240,
+// 10000: 696 and 592; one head, 10000: 100 and 105.
+constexpr int64_t kMostComparing = 16384;
+
+__device__ __forceinline__ void store_mark(float* p, bool m) { *p = m ? 1.f : 0.f; }
+__device__ __forceinline__ void store_mark(uint16_t* p, bool m) { *p = m ? 1 : 0; }
+
+// Thirty-two entries per block, a lane each; its eight warps share the earlier
+// entries, 512 at a time.
+template <class T>
+__global__ void __launch_bounds__(256) mark_kernel(const StepArgs a) {
+  constexpr int kTile = 512;
+  __shared__ longlong2 tile[kTile / 2];
+  __shared__ uint32_t found[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t b0 = static_cast<int64_t>(blockIdx.x) * 32, b = b0 + lane;
+  const int64_t slot = b < a.batch ? a.slots[b] : -1;
+  const int64_t end = b0 + 32 < a.batch ? b0 + 32 : a.batch;
+  auto fetch = [&](int64_t i) { return i < end ? a.slots[i] : -1; };
+  int64_t next0 = fetch(tid), next1 = fetch(tid + 256);
+  bool twice = false;
+  for (int64_t i0 = 0; i0 < end; i0 += kTile) {
+    __syncthreads();
+    int64_t* t = reinterpret_cast<int64_t*>(tile);
+    t[tid] = next0;
+    t[tid + 256] = next1;
+    __syncthreads();
+    next0 = fetch(i0 + kTile + tid);
+    next1 = fetch(i0 + kTile + 256 + tid);
+    if (i0 + kTile <= b0) {  // all of them earlier than all of the block's
+#pragma unroll 8
+      for (int j = warp; j < kTile / 2; j += 8) {
+        const longlong2 s = tile[j];
+        twice |= s.x == slot || s.y == slot;
+      }
+    } else {
+      for (int j = warp; j < kTile / 2; j += 8) {
+        const longlong2 s = tile[j];
+        twice |= (s.x == slot && i0 + 2 * j < b) || (s.y == slot && i0 + 2 * j + 1 < b);
+      }
+    }
+  }
+  const uint32_t m = __ballot_sync(0xFFFFFFFFu, twice);
+  if (lane == 0) found[warp] = m;
+  __syncthreads();
+  uint32_t all = 0u;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) all |= found[w];
+  for (int e = tid; e < 32 * a.heads; e += 256) {
+    const int64_t c = b0 + e / a.heads;
+    if (c < a.batch)
+      store_mark(static_cast<T*>(a.out) + (c * a.heads + e % a.heads) * a.dv, (all >> (e / a.heads)) & 1u);
+  }
+}
+
 
 template <class T>
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
@@ -173,12 +233,10 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = load_f(vp + c);
   }
-  // Of entries with equal slots the first is taken, a later one raises the
-  // flag.  The earlier entries are looked through while the state arrives
-  // (eight heads of 64 x 64: 1000 entries 61 us with slots, 56 without; 10000
-  // entries 667 and 503, by reading the slots from L2).
   bool twice = false;
-  if (a.slots != nullptr && in_pool) {
+  if (a.marked) {
+    twice = static_cast<const T*>(a.out)[(b * a.heads + h) * a.dv] != T(0);
+  } else if (a.slots != nullptr && in_pool) {
 #pragma unroll 4
     for (int64_t i = tid; i < b; i += kStepThreads) twice |= a.slots[i] == slot;
   }
@@ -552,13 +610,20 @@ sa_status sa_linear_attention_step(const void* q, int64_t q_row, int64_t q_head,
   const sa_status dev = sa::on_sm100();
   if (dev != SA_OK) return dev;
   sa::StepArgs a = {iq, ik, iv, log_decay, slots, batch, states, state, out, heads, d_k, d_v, 0,
-                    scale, device_flags};
+                    scale, device_flags, 0};
   // Whole state rows per block when there are two blocks for every SM (of
   // 148); else 32 columns per block, which gives up to eight times as many.
   const int all4 = d_v / 4;
   a.cols4 = batch * heads >= 296 ? all4 : all4 < 8 ? all4 : 8;
   const dim3 grid(static_cast<unsigned>(batch * heads), static_cast<unsigned>((all4 + a.cols4 - 1) / a.cols4));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (slots != nullptr && batch * heads > sa::kMostComparing) {  // (whole rows per block: one mark per head)
+    a.marked = 1;
+    const unsigned blocks = static_cast<unsigned>((batch + 31) / 32);
+    if (dtype == SA_BF16) sa::mark_kernel<uint16_t><<<blocks, 256, 0, st>>>(a);
+    else sa::mark_kernel<float><<<blocks, 256, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
+  }
   if (dtype == SA_BF16) sa::step_kernel<uint16_t><<<grid, sa::kStepThreads, 0, st>>>(a);
   else sa::step_kernel<float><<<grid, sa::kStepThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
