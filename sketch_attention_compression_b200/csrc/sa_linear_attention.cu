@@ -1,7 +1,6 @@
 // Linear attention with a decay per head: the C entry points, the CUDA-core
 // scan and the single-step kernel.  The formulas are in sa_linear_attention.h.
 #include <cuda_bf16.h>
-#include <float.h>
 #include <math.h>
 
 #include "sa.h"
@@ -190,7 +189,6 @@ __global__ void __launch_bounds__(256) mark_kernel(const StepArgs a) {
   }
 }
 
-
 template <class T>
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
   __shared__ float sq[kStepMaxWidth], sk[kStepMaxWidth];
@@ -206,13 +204,6 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
   const int64_t slot = a.slots != nullptr ? a.slots[b] : b;
   const bool padded = slot < 0, past = slot >= a.states, in_pool = !padded && !past;
   const float gd = a.log_decay[h];
-  // The decay with its rounding error, which has one sign at every step and
-  // would add up over the horizon of a state that is advanced row by row.
-  const double w = exp(static_cast<double>(usable_decay(gd)));
-  const float l = static_cast<float>(w), ll = static_cast<float>(w - l);
-  auto next = [&](float x, float kv) {  // (an infinite x times ll = 0 would be NaN)
-    return fmaf(l, x, fmaf(ll, fminf(fmaxf(x, -FLT_MAX), FLT_MAX), kv));
-  };
   float* st = a.state + (((in_pool ? slot : 0) * a.heads + h) * a.dk) * a.dv + col;
   const T* vp = static_cast<const T*>(a.v.p) + b * a.v.row + h * a.v.head + col;
   float v[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -225,14 +216,18 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
     }
   };
   if (in_pool) fetch(g);
-  for (int i = tid; i < a.dk; i += kStepThreads) {
-    sq[i] = load_f(static_cast<const T*>(a.q.p) + b * a.q.row + h * a.q.head + i);
-    sk[i] = load_f(static_cast<const T*>(a.k.p) + b * a.k.row + h * a.k.head + i);
+  static_assert(kStepMaxWidth <= kStepThreads, "an element of q and k per thread");
+  float qt = 0.f, kt = 0.f;
+  if (tid < a.dk) {
+    qt = load_f(static_cast<const T*>(a.q.p) + b * a.q.row + h * a.q.head + tid);
+    kt = load_f(static_cast<const T*>(a.k.p) + b * a.k.row + h * a.k.head + tid);
   }
   if (live) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = load_f(vp + c);
   }
+  sq[tid] = qt;
+  sk[tid] = kt;
   bool twice = false;
   if (a.marked) {
     twice = static_cast<const T*>(a.out)[(b * a.heads + h) * a.dv] != T(0);
@@ -240,6 +235,17 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
 #pragma unroll 4
     for (int64_t i = tid; i < b; i += kStepThreads) twice |= a.slots[i] == slot;
   }
+  // The decay with its rounding error, which has one sign at every step and
+  // would add up over the horizon of a state that is advanced row by row: 1 +
+  // expm1 as a sum of two where the horizon is longer than two rows.  Rounded
+  // down, so that the error's share of an infinite state has its sign, and
+  // never 0 while the decay is not.  Taken while the loads are under way.
+  const float gu = usable_decay(gd), m = expm1f(gu);
+  float e = expf(gu);
+  asm("" : "+f"(e));
+  const float l1 = __fadd_rd(1.f, m);
+  const float l = gu > -0.5f ? l1 : e;
+  const float ll = fmaxf(gu > -0.5f ? m - (l1 - 1.f) : 0.f, __fmul_ru(l, 0x1p-100f));
   twice = __syncthreads_or(twice) != 0;
   T* out = static_cast<T*>(a.out) + (b * a.heads + h) * a.dv + col;
   if (padded || past || twice) {
@@ -249,6 +255,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const StepArgs a) {
     return;
   }
   if (!(gd <= 0.f) && tid == 0 && a.flags != nullptr) atomicOr(a.flags, SA_DEVFLAG_DECAY);
+  auto next = [&](float x, float kv) { return fmaf(l, x, fmaf(ll, x, kv)); };
   for (int r0 = g; r0 < a.dk; r0 += kStepBatch * groups) {
     if (r0 != g) fetch(r0);
 #pragma unroll

@@ -48,3 +48,22 @@ def test_an_infinite_state_stays_infinite():
     linear_attention_step(state, one, one, one, g, 1.0)
     assert (state[:, :, 0] == float("inf")).all() and (state[:, :, 1] == -float("inf")).all()
     assert torch.isfinite(state[:, :, 2]).all()
+
+
+def test_a_state_without_decay_adds_one_rounding():
+    """S + k v is one product and one sum: ties go to the even neighbour in
+    either direction, and k = 0 leaves every bit."""
+    import torch
+    from sketch_attention_compression_b200 import linear_attention_step
+    big = 2.0 ** 23
+    state = torch.tensor([big, big + 1, -big, -big - 1, 1e-38, -3e38, 0.0, 1.0]).cuda()
+    state = state.view(1, 1, 8, 1).expand(1, 1, 8, 4).contiguous()
+    before = state.clone()
+    k = torch.tensor([0.5, 0.5, 0.5, 0.5, 0.0, 0.0, 0.25, 0.0]).cuda().view(1, 1, 8)
+    one, zero = torch.ones((1, 1, 4), device="cuda"), torch.zeros(1, device="cuda")
+    linear_attention_step(state, k, k, one, zero, 1.0)
+    want = before.double() + k.double().view(1, 1, 8, 1)
+    assert torch.equal(state, want.float())  # (rounds once, to nearest even)
+    again = state.clone()
+    linear_attention_step(again, k, torch.zeros_like(k), one, zero, 1.0)
+    assert torch.equal(again, state)
