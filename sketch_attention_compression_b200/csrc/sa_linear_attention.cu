@@ -301,6 +301,14 @@ bool input_ok(const ScanInput& in, int heads, int d, size_t elem) {
          (heads == 1 || in.head >= d);
 }
 
+// True if the rows of `in` may meet [out, out + bytes).
+bool may_meet(const ScanInput& in, int64_t rows, int heads, int d, size_t elem, const void* out,
+              size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(in.p), o = reinterpret_cast<uintptr_t>(out);
+  const int64_t last = (rows - 1) * in.row + (heads - 1) * in.head + d;  // elements
+  return a < o + bytes && o < a + static_cast<uintptr_t>(last) * elem;
+}
+
 // A stride that no element needs (one head, one row) as a dense tensor has it.
 ScanInput dense_where_free(ScanInput in, int64_t rows, int heads, int d) {
   if (heads == 1) in.head = d;
@@ -624,7 +632,12 @@ sa_status sa_linear_attention_step(const void* q, int64_t q_row, int64_t q_head,
   a.cols4 = batch * heads >= 296 ? all4 : all4 < 8 ? all4 : 8;
   const dim3 grid(static_cast<unsigned>(batch * heads), static_cast<unsigned>((all4 + a.cols4 - 1) / a.cols4));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (slots != nullptr && batch * heads > sa::kMostComparing) {  // (whole rows per block: one mark per head)
+  // Marks need an output of their own (and whole rows per block: one a head).
+  const size_t out_bytes = static_cast<size_t>(batch) * heads * d_v * e;
+  if (slots != nullptr && batch * heads > sa::kMostComparing &&
+      !sa::may_meet(iq, batch, heads, d_k, e, out, out_bytes) &&
+      !sa::may_meet(ik, batch, heads, d_k, e, out, out_bytes) &&
+      !sa::may_meet(iv, batch, heads, d_v, e, out, out_bytes)) {
     a.marked = 1;
     const unsigned blocks = static_cast<unsigned>((batch + 31) / 32);
     if (dtype == SA_BF16) sa::mark_kernel<uint16_t><<<blocks, 256, 0, st>>>(a);

@@ -92,3 +92,19 @@ def test_many_entries_with_slots(batch, dtype):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(both, out) and torch.equal(again, state)
+
+
+@pytest.mark.parametrize("batch", [40, 5600])
+def test_a_step_whose_output_replaces_v(batch):
+    """An entry's output may take its v's place, however equal slots are found."""
+    import torch
+    from sketch_attention_compression_b200 import linear_attention_step
+    gen = torch.Generator().manual_seed(batch)
+    q, k, v = (torch.randn((batch, 3, 8), generator=gen).cuda() for _ in range(3))
+    s0, g = torch.randn((batch, 3, 8, 8), generator=gen).cuda(), torch.tensor([-0.1, 0.0, -2.0]).cuda()
+    slots = torch.randperm(batch, generator=gen).cuda()
+    slots[7] = slots[3]
+    one, two = s0.clone(), s0.clone()
+    want = linear_attention_step(one, q, k, v, g, 0.5, slots=slots)
+    got = linear_attention_step(two, q, k, v, g, 0.5, slots=slots, out=v)
+    assert got.data_ptr() == v.data_ptr() and torch.equal(got, want) and torch.equal(one, two)
