@@ -53,7 +53,7 @@
 // such a value in its future.  An output whose O1 is not finite although the
 // state's share is no NaN is summed again over the rows that it may see
 // (sum_again): in the first chunk of a user and head that holds such a value,
-// as the state carries it into every later one.
+// and in later ones only for columns that the state has not made NaN by then.
 #include <cuda_bf16.h>
 
 #include "sa.h"
